@@ -12,6 +12,10 @@ plan / execute / free sequence of the pages (nvmath-python's Matmul as described
     dx, aux = dp.execute()        # aux["drelu_bgrad"]: float32 bias gradient
     p.free(); dp.free()
 
+The 8-bit block-scaled products and the expert (mixture-of-experts) operators are plain functions: see
+fp8.py (quantize_fp8, matmul_fp8, grouped_matmul_fp8, grouped_wgrad_fp8) and experts.py (expert_order,
+expert_dispatch, expert_combine, expert_combine_backward).
+
 The library is loaded from this package directory; if it has not been built the import
 of the library fails loudly (there is no fallback).
 """
@@ -20,8 +24,11 @@ import os
 
 import torch
 
+from ._operators import SIGNATURES
+
 __all__ = ["Plan", "EPError", "EPILOGS", "lib", "library_path", "abi_version", "num_tile_cfgs", "validate_operands",
-           "describe_plan"]
+           "describe_plan", "quantize_fp8", "matmul_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8", "ExpertOrder",
+           "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # EP_LIBRARY names another build of the same library (the host-sanitizer build the CPU tests use)
@@ -101,6 +108,9 @@ def lib():
                                        ctypes.POINTER(ep_epilog_io), ctypes.POINTER(ep_options), ctypes.c_int,
                                        ctypes.c_char_p, ctypes.c_size_t]
         L.ep_plan_describe.restype = ctypes.c_int
+        for name, args in SIGNATURES.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -378,3 +388,8 @@ class Plan:
             self.free()
         except Exception:
             pass
+
+
+# 8-bit block-scaled products and expert operators (they use the binding above)
+from .experts import ExpertOrder, expert_combine, expert_combine_backward, expert_dispatch, expert_order  # noqa: E402
+from .fp8 import grouped_matmul_fp8, grouped_wgrad_fp8, matmul_fp8, quantize_fp8  # noqa: E402

@@ -1,0 +1,104 @@
+"""What the 8-bit and expert operators share: the C ABI's signatures, argument checks, streams."""
+import ctypes
+from functools import wraps
+
+import torch
+
+P, I64, INT, SIZE = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+
+SIGNATURES = {
+    "ep_quantize_fp8": [P, I64, I64, I64, INT, INT, INT, P, I64, P, P],
+    "ep_matmul_fp8_workspace": [I64, I64, I64, P],
+    "ep_matmul_fp8": [I64, I64, I64, P, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, INT, P, SIZE, P],
+    "ep_grouped_matmul_fp8": [I64, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, I64, P, I64, I64, I64, P, I64, INT, P],
+    "ep_grouped_wgrad_fp8": [I64, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, INT, P],
+    "ep_expert_order_sizes": [I64, I64, I64, P, P],
+    "ep_expert_order": [P, INT, I64, I64, I64, P, P, P, P, SIZE, P],
+    "ep_expert_dispatch": [P, I64, I64, I64, INT, P, I64, P, I64, P, I64, P, P],
+    "ep_expert_combine": [P, I64, I64, I64, INT, P, I64, I64, P, I64, P, I64, P],
+    "ep_expert_combine_backward": [P, I64, I64, I64, INT, P, I64, I64, P, I64, P, P, I64, P, I64, P, P],
+}
+
+ELT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+E4M3 = torch.float8_e4m3fn
+BLOCK = 128
+
+
+def blocks(n):
+    return -(-n // BLOCK)
+
+
+def check(name, t, dtypes, shape, device=None):
+    """Raise ValueError unless t is a tensor of one of dtypes (one, or a container) with this shape
+    (None: any size) on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not dtypes and (isinstance(dtypes, torch.dtype) or t.dtype not in dtypes):
+        want = dtypes if isinstance(dtypes, torch.dtype) else " or ".join(str(d) for d in dtypes)
+        raise ValueError(f"{name} must be {want}, got {t.dtype}")
+    s = t.shape
+    if len(s) != len(shape) or any(w is not None and w != g for w, g in zip(shape, s)):
+        want = tuple("any" if w is None else w for w in shape)
+        raise ValueError(f"{name} must have shape {want}, got {tuple(s)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
+
+
+def unit_columns(name, t):
+    """Row stride of a matrix whose rows are contiguous and apart (ValueError otherwise)."""
+    rows, cols = t.shape[-2], t.shape[-1]
+    if t.stride(-1) != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride, got stride {t.stride()}")
+    ld = t.stride(-2)
+    if rows <= 1:
+        return max(ld, cols)
+    if ld < cols:
+        raise ValueError(f"{name}: row stride {ld} is below the row length {cols}")
+    return ld
+
+
+def contiguous(name, t):
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous, got stride {t.stride()}")
+
+
+def on_device(t):
+    if t.device.type != "cuda":
+        raise ValueError(f"operands must be on a CUDA (HIP) device, got {t.device}")
+
+
+def overlaps(a, b):
+    """Whether two tensors' storage ranges meet (an output must not lie over an input)."""
+    if not a.numel() or not b.numel():
+        return False
+    ends = [t.data_ptr() + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size() for t in (a, b)]
+    return a.data_ptr() < ends[1] and b.data_ptr() < ends[0]
+
+
+def check_out(out, dtype, shape, device, inputs):
+    """Row stride of a given output; it may lie over no input."""
+    check("out", out, dtype, shape, device)
+    for t in inputs:
+        if overlaps(out, t):
+            raise ValueError("out lies over an input")
+    return unit_columns("out", out)
+
+
+def streamed(f):
+    """Adds `stream=None`: with a torch stream, the call's kernels and the tensors it allocates go to
+    that stream.  The launches run with the first tensor's device current."""
+    @wraps(f)
+    def call(first, *args, stream=None, **kw):
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return f(first, *args, **kw)
+        t = first if isinstance(first, torch.Tensor) else None
+        if t is not None and t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
+            with torch.cuda.device(t.device):
+                return f(first, *args, **kw)
+        return f(first, *args, **kw)
+    return call
+
+
+def current_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.device.index)

@@ -36,6 +36,8 @@ FLAGS = [
     "-I", CSRC, "-I", INCLUDE,
 ]
 N_EPI = 11
+FP8_KERNELS = ["fp8_gemm", "fp8_quantize", "experts"]
+HOST_SOURCES = ["ep_api", "fp8_api"]
 REMARKS = ["-Rpass-analysis=kernel-resource-usage"]
 REPORT = os.path.join(BUILD, "resource_usage.json")
 
@@ -110,7 +112,10 @@ def build(verbose=False, jobs=None):
                 tasks.append((inst, obj, [f"-DEP_DT={dt}", f"-DEP_LAY={lay}", f"-DEP_EPI={epi}"]))
     tasks.append((os.path.join(CSRC, "elementwise.hip"), os.path.join(BUILD, "elementwise.o"), []))
     tasks.append((os.path.join(CSRC, "static_scratch.hip"), os.path.join(BUILD, "static_scratch.o"), []))
-    tasks.append((os.path.join(CSRC, "ep_api.cpp"), os.path.join(BUILD, "ep_api.o"), []))
+    for name in FP8_KERNELS:
+        tasks.append((os.path.join(CSRC, name + ".hip"), os.path.join(BUILD, name + ".o"), []))
+    for name in HOST_SOURCES:
+        tasks.append((os.path.join(CSRC, name + ".cpp"), os.path.join(BUILD, name + ".o"), []))
     jobs = jobs or min(16, os.cpu_count() or 4)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         done = list(ex.map(_compile, tasks))
@@ -138,23 +143,25 @@ HOSTSAN_LIB = os.path.join(BUILD, "libep_hostsan.so")
 
 
 def build_host_sanitized(verbose=False):
-    """Host-sanitizer build of the C ABI for the CPU tests: ep_api.cpp (validation, planning,
-    dispatch; host code only) compiled by g++ with AddressSanitizer and UndefinedBehavior-
+    """Host-sanitizer build of the C ABI for the CPU tests: ep_api.cpp and fp8_api.cpp (validation,
+    planning, dispatch; host code only) compiled by g++ with AddressSanitizer and UndefinedBehavior-
     Sanitizer, linked with the kernel objects of the last build() (not instrumented).  Load it
     with EP_LIBRARY pointing here and the sanitizer runtimes in LD_PRELOAD."""
-    src = os.path.join(CSRC, "ep_api.cpp")
-    obj = os.path.join(BUILD, "ep_api_hostsan.o")
     objs = sorted(os.path.join(BUILD, f) for f in os.listdir(BUILD) if f.startswith("gemm_") and f.endswith(".o"))
-    objs += [os.path.join(BUILD, "elementwise.o"), os.path.join(BUILD, "static_scratch.o")]
-    if not all(os.path.exists(o) for o in objs) or len(objs) < 3:
+    objs += [os.path.join(BUILD, f + ".o") for f in ["elementwise", "static_scratch"] + FP8_KERNELS]
+    if not all(os.path.exists(o) for o in objs) or len(objs) < 3 + len(FP8_KERNELS):
         raise RuntimeError("run build() first: the sanitized library links its kernel objects")
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
     san = ["-fsanitize=address,undefined", "-fno-omit-frame-pointer"]
-    gxx_compile = ["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"), "-I", CSRC, "-I", INCLUDE, "-c", src, "-o", obj] + san
-    r = subprocess.run(gxx_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"host-sanitizer compile failed:\n{r.stdout}")
-    gxx_link = ["g++", "-shared", "-o", HOSTSAN_LIB, obj] + objs + ["-L", os.path.join(rocm, "lib"), "-lamdhip64", "-Wl,-rpath," + os.path.join(rocm, "lib")] + san
+    host = []
+    for name in HOST_SOURCES:
+        src, obj = os.path.join(CSRC, name + ".cpp"), os.path.join(BUILD, name + "_hostsan.o")
+        gxx_compile = ["g++", "-std=c++17", "-O1", "-g", "-fPIC", "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"), "-I", CSRC, "-I", INCLUDE, "-c", src, "-o", obj] + san
+        r = subprocess.run(gxx_compile, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"host-sanitizer compile failed:\n{r.stdout}")
+        host.append(obj)
+    gxx_link = ["g++", "-shared", "-o", HOSTSAN_LIB] + host + objs + ["-L", os.path.join(rocm, "lib"), "-lamdhip64", "-Wl,-rpath," + os.path.join(rocm, "lib")] + san
     r = subprocess.run(gxx_link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"host-sanitizer link failed:\n{r.stdout}")

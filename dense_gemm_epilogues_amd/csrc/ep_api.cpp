@@ -1087,3 +1087,30 @@ void describe(const ep_plan_s* h, char* buf, size_t n) {
            h->splits, h->args.tail0, h->workspace_bytes, kern.c_str(), extra.c_str());
 }
 }  // namespace
+
+namespace ep {
+
+int api_fail(int status, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail((ep_status)status, "%s", buf);
+}
+
+void api_clear() { t_last_error.clear(); }
+
+int api_stream(void* stream) {
+  int dev = -1, sdev = -1;
+  const hipError_t he = hipGetDevice(&dev);
+  if (he != hipSuccess) return fail(EP_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(he));
+  ep_status st = stream_device((hipStream_t)stream, &sdev);
+  if (st != EP_OK) return st;
+  if (sdev != dev)
+    return fail(EP_ERR_INVALID_ARG, "the stream's device (%d) is not the current device (%d)", sdev, dev);
+  DevInfo di;
+  return device_info(dev, &di);
+}
+
+}  // namespace ep

@@ -279,6 +279,81 @@ ep_status ep_plan_info(ep_handle h, char* buf, size_t n);
 ep_status ep_plan_describe(const ep_shape* shape, ep_dtype dtype, ep_epilog epilog, const ep_epilog_io* io,
                            const ep_options* opt, int cus, char* buf, size_t n);
 
+/* ---------------------------------------------------------------------------------------------
+ * 8-bit block-scaled products and expert (mixture-of-experts) operators.
+ *
+ * No handle: each call validates its arguments (before any HIP call) and enqueues its kernels on
+ * `stream`, which must belong to the calling thread's current device.  Nothing is allocated and
+ * nothing synchronizes; workspaces are the caller's, so every call can be captured into a graph.
+ * Sizes and strides are in elements.  e4m3 is the 8-bit float with 4 exponent and 3 fraction bits,
+ * no infinities and largest value 448.  Pointers are device pointers, except the size outputs.
+ * ------------------------------------------------------------------------------------------- */
+
+/* element types of activations and outputs */
+typedef enum { EP_ELT_F16 = 0, EP_ELT_BF16 = 1, EP_ELT_F32 = 2 } ep_elt;
+
+/* ep_quantize_fp8: x (m x k, row stride ldx), or with transpose its k x m transpose, as e4m3 values q
+ * (row stride ldq) and one fp32 scale for each block of block_rows (1 or 128) rows by 128 columns of
+ * the result.  With amax the block's largest finite magnitude, at least 2^-90: scale = amax / 448 and
+ * q = e4m3(fp32(v * fp32(448 / amax))), to nearest even; infinities and NaN become NaN.
+ * scale of (row r, block c): block_rows 1: scale[c * rows + r] (columns outermost, as the products read
+ * them); block_rows 128: scale[(r / 128) * blocks + c], blocks = ceil(columns / 128). */
+ep_status ep_quantize_fp8(const void* x, int64_t m, int64_t k, int64_t ldx, int elt, int block_rows, int transpose,
+                          void* q, int64_t ldq, float* scale, void* stream);
+
+/* ep_matmul_fp8: D[i][j] = sum over k of a[i][k] sa(i, k/128) b[j][k] sb(j/128, k/128), summed in fp32
+ * and rounded once to `out`.  a: m x k, b: n x k e4m3, 16-byte aligned, row strides multiples of 16
+ * below 2^23, k a multiple of 16; the last block of 128 may be partly filled.  Scale (i, c) is
+ * sa[i * sa_m + c * sa_k], scale (j, c) sb[j * sb_n + c * sb_k].  The workspace (16-byte aligned, of
+ * ep_matmul_fp8_workspace bytes, possibly none) holds the sums of K ranges where few tiles leave
+ * compute units idle; they are joined in a fixed order. */
+ep_status ep_matmul_fp8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
+ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m,
+                        int64_t sa_k, const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d,
+                        int64_t ldd, int out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ep_grouped_matmul_fp8: the same for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of a
+ * (rows x k) times expert e's b (n x k at b + e * b_e, its scales at sb + e * sb_e).  offsets: experts + 1
+ * whole numbers on the device, ascending from 0; rows from offsets[experts] on become zeros. */
+ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t experts, const int32_t* offsets, const void* a,
+                                int64_t lda, const float* sa, int64_t sa_m, int64_t sa_k, const void* b, int64_t b_e,
+                                int64_t ldb, const float* sb, int64_t sb_e, int64_t sb_n, int64_t sb_k, void* d, int64_t ldd,
+                                int out, void* stream);
+
+/* ep_grouped_wgrad_fp8: the experts' weight gradients.  a (m x rows) and b (n x rows) hold the rows as
+ * columns, with scales per row of a and 128 rows of b by 128 columns; D[e] (m x n, row stride ldd, one
+ * expert m * ldd behind another) = sum over columns r = offsets[e] .. offsets[e + 1] - 1 of
+ * a[.][r] b[.][r] with their scales.  Groups start and end on multiples of 128 (the gradient of one that
+ * does not is NaN); an empty group's gradient is zero. */
+ep_status ep_grouped_wgrad_fp8(int64_t m, int64_t n, int64_t rows, int64_t experts, const int32_t* offsets, const void* a,
+                               int64_t lda, const float* sa, int64_t sa_m, int64_t sa_k, const void* b, int64_t ldb,
+                               const float* sb, int64_t sb_n, int64_t sb_k, void* d, int64_t ldd, int out, void* stream);
+
+/* ep_expert_order: (token, choice) slots sorted by expert, in slot order within an expert, each expert's
+ * rows padded to a multiple of align.  ids: slots expert numbers of id_bytes (4 or 8) bytes; one below 0
+ * or at least `experts` (at most 1024) drops its slot.  pos[slot] = its row, or -1; src[row] = its slot, or
+ * -1 for padding, for all `capacity` rows; offsets[e] = expert e's first row, offsets[experts] = their end.
+ * ep_expert_order_sizes: capacity = slots + min(experts, slots) (align - 1), up to a multiple of align. */
+ep_status ep_expert_order_sizes(int64_t slots, int64_t experts, int64_t align, int64_t* capacity, size_t* workspace_bytes);
+ep_status ep_expert_order(const void* ids, int id_bytes, int64_t slots, int64_t experts, int64_t align, int32_t* pos,
+                          int32_t* src, int32_t* offsets, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ep_expert_dispatch: out[pos[t][j]] = x[t] (tokens x h) for every kept choice j; padding rows (src < 0)
+ * are zeros.  With scale non-null the rows are quantised as ep_quantize_fp8 does with 1 x 128 blocks:
+ * out holds e4m3 values, scale[c * rows + row] their scales (2^-90 / 448 in padding rows). */
+ep_status ep_expert_dispatch(const void* x, int64_t tokens, int64_t h, int64_t ldx, int elt, const int32_t* pos, int64_t topk,
+                             const int32_t* src, int64_t rows, void* out, int64_t ldo, float* scale, void* stream);
+
+/* ep_expert_combine: out[t] = sum over kept choices j, in order, of w[t][j] y[pos[t][j]], in fp32, rounded
+ * once; w may be NULL for ones, which makes it the gradient of ep_expert_dispatch.
+ * ep_expert_combine_backward: dy[pos[t][j]] = w[t][j] dout[t], zeros in padding rows, and
+ * dw[t][j] = y[pos[t][j]] . dout[t] (fp32; 0 for a dropped choice). */
+ep_status ep_expert_combine(const void* y, int64_t rows, int64_t h, int64_t ldy, int elt, const int32_t* pos, int64_t tokens,
+                            int64_t topk, const float* w, int64_t ldw, void* out, int64_t ldo, void* stream);
+ep_status ep_expert_combine_backward(const void* dout, int64_t tokens, int64_t h, int64_t ld_dout, int elt, const void* y,
+                                     int64_t rows, int64_t ldy, const int32_t* pos, int64_t topk, const int32_t* src,
+                                     const float* w, int64_t ldw, void* dy, int64_t ld_dy, float* dw, void* stream);
+
 /* Number of selectable tile configurations (valid ep_options.tile_cfg values). */
 int ep_num_tile_cfgs(void);
 
