@@ -1101,7 +1101,7 @@ int api_fail(int status, const char* fmt, ...) {
 
 void api_clear() { t_last_error.clear(); }
 
-int api_stream(void* stream) {
+int api_stream(void* stream, int* cus) {
   int dev = -1, sdev = -1;
   const hipError_t he = hipGetDevice(&dev);
   if (he != hipSuccess) return fail(EP_ERR_HIP, "hipGetDevice: %s", hipGetErrorString(he));
@@ -1110,7 +1110,9 @@ int api_stream(void* stream) {
   if (sdev != dev)
     return fail(EP_ERR_INVALID_ARG, "the stream's device (%d) is not the current device (%d)", sdev, dev);
   DevInfo di;
-  return device_info(dev, &di);
+  st = device_info(dev, &di);
+  if (cus) *cus = di.cus;
+  return st;
 }
 
 }  // namespace ep

@@ -10,7 +10,7 @@ namespace {
 
 constexpr int64_t kMaxLd8 = (int64_t)1 << 23;  // 256 rows stay inside one 2^31-byte buffer window
 constexpr int64_t kMaxCount = ((int64_t)1 << 31) - 4096;
-constexpr int64_t kMaxScaleStride = (int64_t)1 << 23;
+constexpr int64_t kMaxScaleStride = (int64_t)1 << 21;  // as are 256 rows' scales
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 ep_status done(hipError_t e, const char* what) {
@@ -41,7 +41,8 @@ ep_status check_product(int64_t rows_a, int64_t rows_b, int64_t k, const void* a
   EP_REQUIRE(lda < kMaxLd8 && ldb < kMaxLd8, EP_ERR_UNSUPPORTED, "operand row strides must be below 2^23");
   EP_REQUIRE(aligned(sa, 4) && aligned(sb, 4), EP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
   EP_REQUIRE(sa_m >= 0 && sa_k >= 0 && sb_n >= 0 && sb_k >= 0, EP_ERR_INVALID_ARG, "negative scale stride");
-  EP_REQUIRE(sa_m < kMaxScaleStride, EP_ERR_UNSUPPORTED, "the row stride of a's scales must be below 2^23");
+  EP_REQUIRE(sa_m < kMaxScaleStride, EP_ERR_UNSUPPORTED, "the row stride of a's scales must be below 2^21");
+  EP_REQUIRE(sb_n < ((int64_t)1 << 29), EP_ERR_UNSUPPORTED, "the row stride of b's scales must be below 2^29");
   EP_REQUIRE(ldd >= n, EP_ERR_INVALID_ARG, "output row stride below the row length");
   const ep_status st = check_elt(out);
   if (st != EP_OK) return st;
@@ -109,7 +110,7 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
       p.part = (float*)workspace;
     }
   }
-  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
   if (rows) return done(launch_fp8_rows(GM_MATMUL, out, p, m <= 16 ? 16 : 32, (hipStream_t)stream), "matmul_fp8");
   return done(launch_fp8_tiles(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
 }
@@ -125,8 +126,8 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
   EP_REQUIRE(experts < 65535, EP_ERR_UNSUPPORTED, "at most 65534 experts");
   EP_REQUIRE(aligned(offsets, 4), EP_ERR_INVALID_ARG, "misaligned offsets");
   EP_REQUIRE(b_e >= 0 && sb_e >= 0 && b_e % 16 == 0, EP_ERR_INVALID_ARG, "the expert stride of b must be a multiple of 16");
-  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   Fp8Gemm p{};
+  if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
   p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;
   p.lda = lda; p.ldb = ldb; p.ldd = ldd;
   p.sa_m = sa_m; p.sa_k = sa_k; p.sb_n = sb_n; p.sb_k = sb_k;
@@ -148,8 +149,8 @@ ep_status ep_grouped_wgrad_fp8(int64_t m, int64_t n, int64_t rows, int64_t exper
   EP_REQUIRE(experts >= 1 && offsets, EP_ERR_INVALID_ARG, "at least one expert and its offsets are needed");
   EP_REQUIRE(experts < 65535, EP_ERR_UNSUPPORTED, "at most 65534 experts");
   EP_REQUIRE(aligned(offsets, 4), EP_ERR_INVALID_ARG, "misaligned offsets");
-  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   Fp8Gemm p{};
+  if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
   p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;
   p.lda = lda; p.ldb = ldb; p.ldd = ldd;
   p.sa_m = sa_m; p.sa_k = sa_k; p.sb_n = sb_n; p.sb_k = sb_k;

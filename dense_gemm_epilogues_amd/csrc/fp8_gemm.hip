@@ -64,17 +64,6 @@ __device__ __forceinline__ f32x4 mfma128(const Wide& x, const Wide& y) {
   for (int g = 0; g < 4; ++g) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(x.v[g], y.v[g], c, 0, 0, 0);
   return c;
 }
-template <bool WIDE>
-struct FragOf {
-  typedef i32x8 type;
-  static __device__ __forceinline__ i32x8 of(i32x8 x) { return x; }
-};
-template <>
-struct FragOf<true> {
-  typedef Wide type;
-  static __device__ __forceinline__ Wide of(i32x8 x) { return widen(x); }
-};
-
 __device__ __forceinline__ i32x8 join8(u32x4 a, u32x4 b) {
   return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
@@ -94,11 +83,24 @@ __device__ __forceinline__ void group_rows(const int* offsets, int e, int rows, 
   r1 = clampi(offsets[e + 1], r0, rows);
 }
 
+// v, computed here and not kept in registers from before the loop around it
+__device__ __forceinline__ int here(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// v, made once and held in one register: what it is made of is hidden
+__device__ __forceinline__ int keep(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 __device__ __forceinline__ int wave_scan(int v) {  // inclusive sum over the lanes
+  const int lane = here(lane_id());
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const int u = __shfl_up(v, d);
-    if (lane_id() >= d) v += u;
+    if (lane >= d) v += u;
   }
   return v;
 }
@@ -112,120 +114,520 @@ __device__ __forceinline__ void store_row8(char* d, int n, f32x4 lo, f32x4 hi) {
 // ---------------------------------------------------------------------------------------- tiles
 constexpr int kGroupM = 8;
 
-// BM x BN tiles of D, WGM x WGN waves; both operands go through LDS in a ring of two stages of one
-// scale block (128 bytes a row: one cache line, 8 lanes of 16 bytes), filled by buffer loads that
-// write LDS while the stage before is computed.  16-byte piece c of row r is kept at piece c ^ (r & 7),
-// which the fragment reads (16 rows at one piece per 16 lanes) take without bank conflicts.  Within
-// each 32 rows of b, LDS row 16 u + 4 q + i holds n = 8 q + 4 u + i, so that a lane's values of two
-// neighbouring blocks are 8 neighbouring n: a 16-byte store.
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN, bool WIDE>
+template <class T>
+__device__ __forceinline__ T* global_ptr(T* p) {
+  return (T*)(__attribute__((address_space(1))) T*)(uint64_t)p;
+}
+
+// A kernel's only argument, read from its segment here and not kept in registers from before a loop.
+__device__ __forceinline__ Fp8Gemm args_here() {
+  typedef const __attribute__((address_space(4))) uint32_t* Words;
+  const uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
+  asm volatile("" : "+s"(lo), "+s"(hi));
+  const Words k = (Words)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)hi) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)lo));
+  uint32_t w[sizeof(Fp8Gemm) / 4];
+#pragma unroll
+  for (size_t i = 0; i < sizeof(Fp8Gemm) / 4; ++i) w[i] = k[i];
+  Fp8Gemm p = __builtin_bit_cast(Fp8Gemm, w);
+  // (global, which the compiler can no longer see; flat accesses would count as LDS accesses too, and with
+  // those pending it waits for all fragment reads at once)
+  p.sa = global_ptr(p.sa);
+  p.sb = global_ptr(p.sb);
+  p.d = global_ptr(p.d);
+  p.offsets = global_ptr(p.offsets);
+  return p;
+}
+
+// One BM x BN tile of D and the scale blocks that go into it.
+struct Tile {
+  int m0, mv, n0, nv;      // rows from m0, mv of them; columns from n0, nv of them
+  int kb0, nkb, klen;      // scale blocks from kb0, nkb of them (0: the tile is `fill`); k-values end at klen
+  int part;                // expert, or K range
+  float fill;
+};
+
+// The tiles of a product in the order they are worked on: bands of kGroupM tile rows, column by column,
+// so that neighbours share operand panels; grouped: expert by expert, then the rows behind the last group.
+template <int MODE, int BM, int BN>
+struct Tiles {
+  int count;               // tiles there are
+  int e0 = 0, base = 0;    // grouped: a group to go on from, tile rows before it
+
+  __device__ __forceinline__ explicit Tiles(const Fp8Gemm& p) {
+    if constexpr (MODE == GM_GROUPED) {
+      int total = (p.M - clampi(p.offsets[p.experts], 0, p.M) + BM - 1) / BM;
+      for (int e = 0; e < p.experts; e += 64) {
+        int r0 = 0, r1 = 0;
+        if (e + lane_id() < p.experts) group_rows(p.offsets, e + lane_id(), p.M, r0, r1);
+        total += __shfl(wave_scan((r1 - r0 + BM - 1) / BM), 63);
+      }
+      count = __builtin_amdgcn_readfirstlane(total) * p.tiles_n;
+    } else {
+      count = p.tiles_m * p.tiles_n * (MODE == GM_WGRAD ? p.experts : p.splits);
+    }
+  }
+
+  static __device__ __forceinline__ void place(int tiles_n, int w, int rows, int& tm, int& tn) {
+    const int group = kGroupM * tiles_n, g = w / group, first = g * kGroupM;
+    const int gm = min(rows - first, kGroupM), v = w - g * group;
+    tm = first + v % gm;
+    tn = v / gm;
+  }
+
+  // tile u; for the groups u must not fall from one call to the next
+  __device__ __forceinline__ Tile at(const Fp8Gemm& p, int u) {
+    Tile t;
+    t.part = t.kb0 = 0;
+    t.klen = p.K;
+    t.fill = 0.0f;
+    int tm, tn;
+    if constexpr (MODE == GM_MATMUL) {
+      const int tiles = p.tiles_m * p.tiles_n;
+      t.part = u / tiles;
+      place(p.tiles_n, u - t.part * tiles, p.tiles_m, tm, tn);
+      t.m0 = tm * BM;
+      t.mv = min(BM, p.M - t.m0);
+      t.kb0 = t.part * p.kb_per_split;
+      t.nkb = min(p.kb_per_split, (p.K + kScaleBlock - 1) / kScaleBlock - t.kb0);
+    } else if constexpr (MODE == GM_GROUPED) {
+      int e = -1, first = 0, r0 = 0, r1 = 0;
+      for (; e0 < p.experts; e0 += 64) {
+        int q0 = 0, q1 = 0;
+        if (e0 + lane_id() < p.experts) group_rows(p.offsets, e0 + lane_id(), p.M, q0, q1);
+        const int c = (q1 - q0 + BM - 1) / BM;
+        const int ends = base + wave_scan(c);
+        const uint64_t past = __ballot(ends * p.tiles_n > u);
+        if (past) {
+          const int l = __builtin_ctzll(past);
+          e = e0 + l;
+          first = __shfl(ends - c, l);
+          r0 = __shfl(q0, l);
+          r1 = __shfl(q1, l);
+          break;
+        }
+        base = __builtin_amdgcn_readfirstlane(__shfl(ends, 63));
+      }
+      if (e < 0) {
+        e = p.experts;
+        first = base;
+        r0 = clampi(p.offsets[e], 0, p.M);
+        r1 = p.M;
+      }
+      t.part = __builtin_amdgcn_readfirstlane(e);
+      first = __builtin_amdgcn_readfirstlane(first);
+      r0 = __builtin_amdgcn_readfirstlane(r0);
+      r1 = __builtin_amdgcn_readfirstlane(r1);
+      place(p.tiles_n, u - first * p.tiles_n, (r1 - r0 + BM - 1) / BM, tm, tn);
+      t.m0 = r0 + tm * BM;
+      t.mv = min(BM, r1 - t.m0);
+      t.nkb = t.part == p.experts ? 0 : (p.K + kScaleBlock - 1) / kScaleBlock;
+    } else {
+      const int tiles = p.tiles_m * p.tiles_n;
+      t.part = u / tiles;
+      place(p.tiles_n, u - t.part * tiles, p.tiles_m, tm, tn);
+      t.m0 = tm * BM;
+      t.mv = min(BM, p.M - t.m0);
+      int r0, r1;
+      group_rows(p.offsets, t.part, p.K, r0, r1);
+      r0 = __builtin_amdgcn_readfirstlane(r0);
+      r1 = __builtin_amdgcn_readfirstlane(r1);
+      t.kb0 = r0 / kScaleBlock;
+      t.nkb = r1 / kScaleBlock - t.kb0;
+      t.klen = r1;
+      if ((r0 | r1) % kScaleBlock) {  // such a group has no scales of its own
+        t.nkb = 0;
+        t.fill = __builtin_nanf("");
+      }
+    }
+    t.n0 = tn * BN;
+    t.nv = min(BN, p.N - t.n0);
+    return t;
+  }
+
+};
+
+template <int MODE>
+__device__ __forceinline__ const uint8_t* tile_a(const Fp8Gemm& p, const Tile& t) {
+  return p.a + (int64_t)t.m0 * p.lda + (int64_t)t.kb0 * kScaleBlock;
+}
+template <int MODE>
+__device__ __forceinline__ const uint8_t* tile_b(const Fp8Gemm& p, const Tile& t) {
+  return p.b + (MODE == GM_GROUPED ? (int64_t)t.part * p.b_e : 0) + (int64_t)t.n0 * p.ldb + (int64_t)t.kb0 * kScaleBlock;
+}
+template <int MODE>
+__device__ __forceinline__ const float* tile_sa(const Fp8Gemm& p, const Tile& t) {
+  return p.sa + (int64_t)t.m0 * p.sa_m + (int64_t)t.kb0 * p.sa_k;
+}
+template <int MODE>
+__device__ __forceinline__ const float* tile_sb(const Fp8Gemm& p, const Tile& t, int n) {  // of column n0 + n
+  return p.sb + (MODE == GM_GROUPED ? (int64_t)t.part * p.sb_e : 0) + (int64_t)((t.n0 + n) / kScaleBlock) * p.sb_n + (int64_t)t.kb0 * p.sb_k;
+}
+// element (0, 0) of the tile; experts' gradients and K ranges' parts lie one behind another
+template <int MODE, int OT>
+__device__ __forceinline__ char* tile_d(const Fp8Gemm& p, const Tile& t) {
+  const int64_t row = (int64_t)(MODE == GM_GROUPED ? 0 : t.part) * p.M + t.m0;
+  return (char*)p.d + (row * p.ldd + t.n0) * elt_size(OT);
+}
+
+// a tile without products
+template <int MODE, int OT, int BN>
+__device__ __forceinline__ void fill_tile(const Fp8Gemm& p, const Tile& t) {
+  const f32x4 v = {t.fill, t.fill, t.fill, t.fill};
+  char* d = tile_d<MODE, OT>(p, t);
+  for (int i = here((int)threadIdx.x); i < t.mv * (BN / 8); i += (int)blockDim.x) {
+    const int m = i / (BN / 8), n = i % (BN / 8) * 8;
+    if (n < t.nv) store_row8<OT>(d + (m * p.ldd + n) * elt_size(OT), t.nv - n, v, v);
+  }
+}
+
+// Row of a 16-row block that lane l (of 16) holds: LDS row 16 u + 4 q + i of each 32 holds row 8 q + 4 u + i,
+// so that a lane's values of two neighbouring blocks along n are 8 neighbouring ones.
+__device__ __forceinline__ int row_in(int block, int l) {
+  return (block >> 1) * 32 + (l >> 2) * 8 + (block & 1) * 4 + (l & 3);
+}
+
+// a wave's accumulators to D: in a lane one row of each 16 (in row_in's order, or lane by lane) and 8
+// neighbouring columns
+template <int MODE, int OT, bool PERM, int MT, int NT>
+__device__ __forceinline__ void store_tile(const Fp8Gemm& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
+  const int lane = here(lane_id());
+  char* d = tile_d<MODE, OT>(p, t) + (m_at * p.ldd + n_at) * elt_size(OT);
+  const int n0 = 8 * (lane >> 4);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = PERM ? row_in(i, lane & 15) : i * 16 + (lane & 15);
+    if (m >= t.mv - m_at) continue;
+    char* row = d + (m * p.ldd + n0) * elt_size(OT);
+#pragma unroll
+    for (int j = 0; j < NT; j += 2) {
+      const int left = t.nv - n_at - n0 - j * 16;
+      if (left > 0) store_row8<OT>(row + j * 16 * elt_size(OT), left, acc[i][j], acc[i][j + 1]);
+    }
+  }
+}
+
+// ---- the e4m3 tiles
+// Which of three or four register slots column block j's fragment of b takes, and when it is read: the two
+// last blocks and the next step's first one are held at the same time, a slot is free once its block's MFMAs
+// are issued.
+template <int NT>
+__device__ constexpr int slot_of(int j) {
+  constexpr int eight[8] = {2, 0, 1, 0, 1, 2, 0, 1};
+  return NT == 8 ? eight[j] : j;
+}
+template <int NT>
+__device__ constexpr int read_after(int j) {  // the column block behind whose MFMAs block j is read, -1: the step's start
+  int r = -1;
+  for (int i = 0; i < j; ++i)
+    if (slot_of<NT>(i) == slot_of<NT>(j)) r = i;
+  return r;
+}
+
+template <int NT>
+__device__ constexpr bool read_first(int j) {
+  return read_after<NT>(j) < 0 || read_after<NT>(j) >= NT - 2;
+}
+
+// BM x BN tiles of D, WGM x WGN waves, as many workgroups as fit the chip, each walking its share of the
+// tiles.  Both operands and their scales go through LDS in a ring of S stages of one scale block (128 bytes
+// a row: one cache line, 8 lanes of 16 bytes), filled by loads that write LDS themselves.  16-byte piece c of
+// row r is kept at piece c ^ (r & 7), which the fragment reads (16 rows at one piece per 16 lanes) take
+// without bank conflicts; the rows of each 32 are in row_in's order.
+//
+// Two barriers a step.  Behind the first, after the first column block, every wave holds its fragments of a:
+// the stage's part of a is free, and the loads of the step S ahead go into it.  Behind the second, before the
+// last two blocks, every wave holds what it reads of b as well: the loads of b follow, and the next stage has
+// landed.  So the loads, which take half of the step's time in the address unit, are spread over it.  The last two
+// blocks' MFMAs go row block by row block, each row block's fragment of a followed by the next step's, so the
+// matrix unit does not wait for a step's first reads.  The steps run on from tile to tile: the next tile's
+// operands land while this one's last steps are multiplied.
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
 void fp8_tile_kernel(Fp8Gemm p) {
+#ifdef __HIP_DEVICE_COMPILE__  // (the host's pass drops a body with register constraints it does not know)
+  constexpr int WAVES = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, MT = WTM / 16, NT = WTN / 16;
+  constexpr int OPS = (BM + BN) * 128, STAGE = OPS + WAVES * 256;
+  constexpr int N = MT * NT, R = NT == 8 ? 3 : 4;  // a step's MFMAs; results in flight: the multiply-adds follow 2 MFMAs behind
+  static_assert(BM == 32 * WAVES && BN == 32 * WAVES && WTN <= 128 && 128 % WTN == 0 && BM / 64 < WAVES, "tile");
+  static_assert((NT == 8 || NT == 4) && MT == 4, "schedule");
+  __shared__ __align__(128) char lds[S * STAGE];
+  const int lane = lane_id(), wave = wave_id();
+  const int wm = wave / WGN, wn = wave % WGN;
+  Tiles<MODE, BM, BN> tiles(p);
+  int bid = (int)blockIdx.x;
+  const int blocks = (int)gridDim.x;
+
+  // the next tile with products, the others filled on the way
+  auto next = [&](Tile& t) __attribute__((always_inline)) {
+    const Fp8Gemm q = args_here();
+    t.nkb = 0;
+    while (bid < tiles.count && t.nkb == 0) {
+      t = tiles.at(q, xcd_order(bid, tiles.count));
+      bid += blocks;
+      if (t.nkb == 0) fill_tile<MODE, OT, BN>(q, t);
+    }
+    return t.nkb > 0;
+  };
+
+  // ---- the loads' side: a wave's 32 rows of a and of b, 8 of them a piece, and 64 scales: rows' in the first
+  // BM / 64 waves, the columns' in the next one (the others load some rows' into places of their own)
+  const int piece16 = ((lane & 7) ^ (lane >> 3)) * 16;
+  const bool sb_wave = wave == BM / 64;
+  // a lane's row of piece 0 (pieces are 8 LDS rows, see row_in); the others are row_of(s) behind it.  Rows past
+  // the tile's are past the descriptor's range, which the hardware checks without the scalar offset
+  auto row_of = [](int s) __attribute__((always_inline)) { return 16 * (s & 1) + 4 * (s >> 1); };
+  const int row0 = 8 * (lane >> 5) + ((lane >> 3) & 3);
+  __amdgpu_buffer_rsrc_t ra, rb;
+  int lda = 0, ldb = 0;
+  uint32_t aoff, boff, ak = 0, bk = 0;
+  int lk = 0, lklen = 0, ls_left = 0;  // k of the next step, where k ends, steps of scales to come
+  const float* lsp;
+  int64_t ls_step = 0;
+  uint32_t lsoff;
+  auto load_tile = [&](const Tile& t) __attribute__((always_inline)) {
+    const Fp8Gemm q = args_here();
+    lda = (int)q.lda;
+    ldb = (int)q.ldb;
+    const int rows_a = t.mv - wave * 32, rows_b = t.nv - wave * 32;  // (at most 0: the wave loads zeros)
+    lk = 0;
+    lklen = min(t.klen - t.kb0 * kScaleBlock, t.nkb * kScaleBlock);
+    ra = rsrc_of(tile_a<MODE>(q, t) + (int64_t)(wave * 32) * lda, rows_a > 0 ? (int64_t)(rows_a - 1) * lda + lklen : 0);
+    rb = rsrc_of(tile_b<MODE>(q, t) + (int64_t)(wave * 32) * ldb, rows_b > 0 ? (int64_t)(rows_b - 1) * ldb + lklen : 0);
+    aoff = (uint32_t)(row0 * lda + piece16);
+    boff = (uint32_t)(row0 * ldb + piece16);
+    lsp = sb_wave ? tile_sb<MODE>(q, t, 0) : tile_sa<MODE>(q, t);
+    lsoff = (uint32_t)(sb_wave ? min(lane, (t.nv - 1) / kScaleBlock) * (int)q.sb_n
+                               : min(wave % (BM / 64) * 64 + lane, t.mv - 1) * (int)q.sa_m) * 4;
+    ls_step = sb_wave ? q.sb_k : q.sa_k;
+    ls_left = t.nkb;
+  };
+  auto load_k = [&]() __attribute__((always_inline)) {  // (k is a multiple of 16: pieces are whole or absent)
+    const bool in = lk + piece16 < lklen;
+    ak = in ? aoff : kOOB;
+    bk = in ? boff : kOOB;
+  };
+  auto load_a = [&](int stage, int s) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        ra, (__attribute__((address_space(3))) void*)(lds + stage * STAGE + (wave * 4 + s) * 1024), 16,
+        (int)(ak + row_of(s) * lda), lk, 0, 0);
+  };
+  auto load_b = [&](int stage, int s) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rb, (__attribute__((address_space(3))) void*)(lds + stage * STAGE + BM * 128 + (wave * 4 + s) * 1024), 16,
+        (int)(bk + row_of(s) * ldb), lk, 0, 0);
+  };
+  auto load_scales = [&](int stage) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc_of(lsp, 0x7fffffff), (__attribute__((address_space(3))) void*)(lds + stage * STAGE + OPS + wave * 256), 4, (int)lsoff, 0, 0, 0);
+  };
+  auto load_done = [&]() __attribute__((always_inline)) {
+    lk += kScaleBlock;
+    if (--ls_left > 0) lsp += ls_step;
+  };
+
+  // ---- the products' side
+  const int frow = (lane & 15) * 128 + ((lane >> 4) ^ (lane & 7)) * 16;
+  const int va = keep(wm * WTM * 128 + frow), vb = keep(BM * 128 + wn * WTN * 128 + frow);
+  const int vt = keep(OPS + (wm * WTM + row_in(0, lane & 15)) * 4);
+  // block's fragment of the operand whose lane offset in this stage is `at`
+  auto frag = [&](int at, int block) __attribute__((always_inline)) {
+    return join8(*(const u32x4*)(lds + at + block * 2048), *(const u32x4*)(lds + (at ^ 64) + block * 2048));
+  };
+  f32x4 acc[MT][NT], pr[R];
+  i32x8 fa[MT], fb[NT == 8 ? 3 : 4];
+  float t[MT], tn[MT], tb = 0.0f, t_last = 0.0f;
+  auto read_scales = [&](int at) __attribute__((always_inline)) {
+    const char* q = lds + at + vt;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) tn[i] = *(const float*)(q + row_in(i, 0) * 4);
+    tb = *(const float*)(lds + at + OPS + (BM + wn * WTN / kScaleBlock) * 4);
+  };
+  // the step's MFMAs in order: column blocks, the last two of them row block by row block
+  auto mfma = [&](int x) __attribute__((always_inline)) {
+    constexpr int H = MT * (NT - 2);
+    const int i = x < H ? x % MT : (x - H) / 2, j = x < H ? x / MT : NT - 2 + (x - H) % 2;
+    pr[x % R] = mfma128(fb[slot_of<NT>(j)], fa[i]);
+  };
+  auto add = [&](int x) __attribute__((always_inline)) {
+    constexpr int H = MT * (NT - 2);
+    const int i = x < H ? x % MT : (x - H) / 2, j = x < H ? x / MT : NT - 2 + (x - H) % 2;
+    acc[i][j] += pr[x % R] * t[i];
+  };
+  // a step's last product is added behind the next step's first MFMA
+  auto add_last = [&]() __attribute__((always_inline)) { acc[MT - 1][NT - 1] += pr[(N - 1) % R] * t_last; };
+  auto clear = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    pr[(N - 1) % R] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    t_last = 0.0f;
+  };
+
+  Tile cur, ahead;
+  if (!next(cur)) return;
+  clear();
+  load_tile(cur);
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    load_scales(s);
+    load_k();
+#pragma unroll
+    for (int x = 0; x < 4; ++x) load_a(s, x);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) load_b(s, x);
+    load_done();
+  }
+  constexpr int WAIT0 = (S - 1) * 9, WAIT = (S - 2) * 9 + 5;
+  __builtin_amdgcn_s_waitcnt((WAIT0 & 15) | ((WAIT0 >> 4) << 14) | 0x0f70);
+  asm volatile("s_barrier" ::: "memory");
+  // what a step finds in registers, or on its way: all of a, the first block of b, the scales' products
+  read_scales(0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) fa[i] = frag(va, i);
+  fb[slot_of<NT>(0)] = frag(vb, 0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) t[i] = tn[i] * tb;
+
+  bool more = false, done = false;
+  int step = 0, steps = max(cur.nkb, S), stage = 0;  // (a tile of fewer steps than stages gets empty ones)
+  auto steps_on = [&]() __attribute__((always_inline)) {  // (the other waves only load)
+    return (wm * WTM < cur.mv) & (wn * WTN < cur.nv) ? cur.nkb : 0;
+  };
+  int on = steps_on();
+  while (!done) {
+    const int stage1 = stage + 1 == S ? 0 : stage + 1;
+    if (__builtin_expect(step + S == steps, 0)) {  // the loads go on to the next tile, or to nothing
+      more = next(ahead);
+      if (more) load_tile(ahead);
+      else lklen = 0;
+      __builtin_amdgcn_s_waitcnt(0xc07f);  // (lgkmcnt: with scalar loads pending the compiler could not count fragment reads)
+    }
+    load_k();
+    // second barrier: this wave's loads of the next stage have landed, and it holds all it reads of this one
+    // (a wait visible to the compiler's own counting); behind it that holds for everyone
+    auto barrier = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_s_waitcnt((WAIT & 15) | ((WAIT >> 4) << 14) | 0x0070);
+      asm volatile("s_barrier" ::: "memory");
+    };
+    if (__builtin_expect(step < on, 1)) {
+      const int b_at = keep(vb + stage * STAGE);
+#pragma unroll
+      for (int j = 1; j < NT; ++j)
+        if (read_first<NT>(j)) fb[slot_of<NT>(j)] = frag(b_at, j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < NT - 2; ++j) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          const int x = j * MT + i;
+          mfma(x);
+          __builtin_amdgcn_sched_barrier(0);
+          if (x == 0) add_last();
+          if (x >= 2) add(x - 2);
+          __builtin_amdgcn_sched_barrier(0);
+          // the loads of a, over the blocks left before the last two
+          if (j > 0 && (NT == 4 || i == 1)) {
+            if (NT == 4 ? i == 0 : j == 1) load_scales(stage);
+            if (NT == 4) load_a(stage, i);
+            else if (j > 1) load_a(stage, j - 2);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+#pragma unroll
+        for (int n = j + 1; n < NT; ++n)
+          if (read_after<NT>(n) == j && !read_first<NT>(n)) fb[slot_of<NT>(n)] = frag(b_at, n);
+        __builtin_amdgcn_sched_barrier(0);
+        if (j == 0) asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      barrier();
+      read_scales(stage1 * STAGE);
+      const int a_next = keep(va + stage1 * STAGE);
+      fb[slot_of<NT>(0)] = frag(vb + stage1 * STAGE, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int x = MT * (NT - 2) + 2 * i + h;
+          mfma(x);
+          __builtin_amdgcn_sched_barrier(0);
+          add(x - 2);
+          __builtin_amdgcn_sched_barrier(0);
+          if (h == 0) load_b(stage, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        fa[i] = frag(a_next, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      add(N - 2);
+      t_last = t[MT - 1];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) t[i] = tn[i] * tb;
+    } else {
+      __builtin_amdgcn_s_waitcnt(0xc07f);
+      asm volatile("s_barrier" ::: "memory");
+      load_scales(stage);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) load_a(stage, x);
+      barrier();
+      read_scales(stage1 * STAGE);
+      fb[slot_of<NT>(0)] = frag(vb + stage1 * STAGE, 0);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) load_b(stage, x);
+      const int a_next = keep(va + stage1 * STAGE);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i] = frag(a_next, i);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) t[i] = tn[i] * tb;
+    }
+    load_done();
+    stage = stage1;
+    if (__builtin_expect(++step == steps, 0)) {
+      // (the last loads write LDS too: not after the workgroup has left it)
+      if (!more) __builtin_amdgcn_s_waitcnt(0x0070);
+      add_last();
+      store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
+      done = !more;
+      clear();
+      cur = ahead;
+      step = 0;
+      steps = max(cur.nkb, S);
+      on = steps_on();
+    }
+  }
+#endif
+}
+
+// ---- the same with operands widened to fp16: one tile a workgroup, 128 x 128 so that two of them share a
+// compute unit and one's loads pass behind the other's products.
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN>
+__global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
+void fp8_wide_kernel(Fp8Gemm p) {
   constexpr int WAVES = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, MT = WTM / 16, NT = WTN / 16;
   constexpr int SLOTS = (BM + BN) / 8, PER_WAVE = SLOTS / WAVES, STAGE = (BM + BN) * 128;
   static_assert(SLOTS % WAVES == 0 && (BM / 8) % PER_WAVE == 0 && NT % 2 == 0 && WTN <= 128 && 128 % WTN == 0, "tile");
   __shared__ __align__(128) char lds[2 * STAGE];
   const int lane = lane_id(), wave = wave_id();
   const int wm = wave / WGN, wn = wave % WGN;
-
-  // ---- which tile
-  int m0, mv, n0, kb0, kb1, klen;  // rows from m0, mv of them; columns from n0; scale blocks kb0 .. kb1
-  const uint8_t *a = p.a, *b = p.b;
-  const float *sa = p.sa, *sb = p.sb;
-  char* d = (char*)p.d;
-  bool zero_only = false, poison = false;
-  if constexpr (MODE == GM_MATMUL) {
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int split = (int)blockIdx.x / tiles;
-    const int t = xcd_order((int)blockIdx.x - split * tiles, tiles);
-    const int group = kGroupM * p.tiles_n, g = t / group, first = g * kGroupM;
-    const int gm = min(p.tiles_m - first, kGroupM), w = t - g * group;
-    m0 = (first + w % gm) * BM;
-    n0 = (w / gm) * BN;
-    mv = min(BM, p.M - m0);
-    kb0 = split * p.kb_per_split;
-    kb1 = min(kb0 + p.kb_per_split, (p.K + kScaleBlock - 1) / kScaleBlock);
-    klen = p.K;
-    if (p.splits > 1) d = (char*)(p.part + (int64_t)split * p.M * p.N);
-  } else if constexpr (MODE == GM_GROUPED) {
-    // tiles of the groups in order, then those of the rows behind the last group, which are zeroed
-    int base = 0, total = 0;
-    const int last = clampi(p.offsets[p.experts], 0, p.M);
-    const int tail = (p.M - last + BM - 1) / BM;
-    for (int e0 = 0; e0 < p.experts; e0 += 64) {
-      int r0 = 0, r1 = 0;
-      if (e0 + lane < p.experts) group_rows(p.offsets, e0 + lane, p.M, r0, r1);
-      total += __shfl(wave_scan((r1 - r0 + BM - 1) / BM), 63);
-    }
-    const int tiles = (total + tail) * p.tiles_n;
-    if ((int)blockIdx.x >= tiles) return;
-    const int t = xcd_order((int)blockIdx.x, tiles);
-    int e = p.experts, first = total, cnt = tail, r0 = last, r1 = p.M;
-    for (int e0 = 0; e0 < p.experts; e0 += 64) {
-      int q0 = 0, q1 = 0;
-      if (e0 + lane < p.experts) group_rows(p.offsets, e0 + lane, p.M, q0, q1);
-      const int c = (q1 - q0 + BM - 1) / BM;
-      const int ends = base + wave_scan(c);
-      const uint64_t past = __ballot(ends * p.tiles_n > t);
-      if (past) {
-        const int l = __builtin_ctzll(past);
-        e = e0 + l;
-        cnt = __shfl(c, l);
-        first = __shfl(ends, l) - cnt;
-        r0 = __shfl(q0, l);
-        r1 = __shfl(q1, l);
-        break;
-      }
-      base = __shfl(ends, 63);
-    }
-    e = __builtin_amdgcn_readfirstlane(e);
-    cnt = __builtin_amdgcn_readfirstlane(cnt);
-    first = __builtin_amdgcn_readfirstlane(first);
-    r0 = __builtin_amdgcn_readfirstlane(r0);
-    r1 = __builtin_amdgcn_readfirstlane(r1);
-    const int w = t - first * p.tiles_n;
-    m0 = r0 + (w % cnt) * BM;
-    n0 = (w / cnt) * BN;
-    mv = min(BM, r1 - m0);
-    zero_only = e == p.experts;
-    if (!zero_only) {
-      b += (int64_t)e * p.b_e;
-      sb += (int64_t)e * p.sb_e;
-    }
-    kb0 = 0;
-    kb1 = zero_only ? 0 : (p.K + kScaleBlock - 1) / kScaleBlock;
-    klen = p.K;
-  } else {
-    const int tiles = p.tiles_m * p.tiles_n;
-    const int u = xcd_order((int)blockIdx.x, tiles * p.experts);
-    const int e = u / tiles, t = u - e * tiles;
-    const int group = kGroupM * p.tiles_n, g = t / group, first = g * kGroupM;
-    const int gm = min(p.tiles_m - first, kGroupM), w = t - g * group;
-    m0 = (first + w % gm) * BM;
-    n0 = (w / gm) * BN;
-    mv = min(BM, p.M - m0);
-    int r0, r1;
-    group_rows(p.offsets, e, p.K, r0, r1);
-    r0 = __builtin_amdgcn_readfirstlane(r0);
-    r1 = __builtin_amdgcn_readfirstlane(r1);
-    // a group that does not start and end on scale blocks has no scales of its own: NaN
-    poison = (r0 | r1) % kScaleBlock != 0;
-    kb0 = r0 / kScaleBlock;
-    kb1 = poison ? kb0 : r1 / kScaleBlock;
-    klen = r1;
-    d += (int64_t)e * p.M * p.ldd * elt_size(OT);
+  Tiles<MODE, BM, BN> tiles(p);
+  if ((int)blockIdx.x >= tiles.count) return;
+  const Tile tile = tiles.at(p, xcd_order((int)blockIdx.x, tiles.count));
+  if (tile.nkb <= 0) {
+    fill_tile<MODE, OT, BN>(p, tile);
+    return;
   }
-  const int nv = min(BN, p.N - n0);
-  a += (int64_t)m0 * p.lda + (int64_t)kb0 * kScaleBlock;
-  b += (int64_t)n0 * p.ldb + (int64_t)kb0 * kScaleBlock;
-  klen -= kb0 * kScaleBlock;
-  const int nkb = kb1 - kb0;
+  const int mv = tile.mv, nv = tile.nv, nkb = tile.nkb;
+  const int klen = tile.klen - tile.kb0 * kScaleBlock;
 
   // ---- loads: slot s of a stage is 8 rows; a wave's slots are neighbours and all of one operand
   const bool a_side = wave * PER_WAVE < BM / 8;
   const int64_t ld = a_side ? p.lda : p.ldb;
   const int rows = a_side ? mv : nv;
-  const __amdgpu_buffer_rsrc_t rs = rsrc_of(a_side ? a : b, (int64_t)(rows - 1) * ld + klen);
+  const __amdgpu_buffer_rsrc_t rs = rsrc_of(a_side ? tile_a<MODE>(p, tile) : tile_b<MODE>(p, tile), (int64_t)(rows - 1) * ld + klen);
   const int piece = (lane & 7) ^ (lane >> 3);
   uint32_t voff[PER_WAVE];
 #pragma unroll
@@ -249,9 +651,9 @@ void fp8_tile_kernel(Fp8Gemm p) {
                                                (int)(in ? voff[s] : kOOB), k0, 0, 0);
   };
   // ---- scales of this wave's rows and its 128 columns
-  const float* sap = sa + (int64_t)m0 * p.sa_m + (int64_t)kb0 * p.sa_k;
-  const float* sbp = sb + (int64_t)((n0 + wn * WTN) / kScaleBlock) * p.sb_n + (int64_t)kb0 * p.sb_k;
-  const bool n_on = n0 + wn * WTN < p.N;
+  const float* sap = tile_sa<MODE>(p, tile);
+  const bool n_on = wn * WTN < nv;
+  const float* sbp = tile_sb<MODE>(p, tile, n_on ? wn * WTN : 0);
   uint32_t soff[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) soff[i] = (uint32_t)(min(wm * WTM + i * 16 + (lane & 15), mv - 1) * p.sa_m);
@@ -260,7 +662,7 @@ void fp8_tile_kernel(Fp8Gemm p) {
     const float* q = sap + (int64_t)kb * p.sa_k;
 #pragma unroll
     for (int i = 0; i < MT; ++i) sn[i] = q[soff[i]];
-    sbn = n_on ? sbp[(int64_t)kb * p.sb_k] : 0.0f;
+    sbn = sbp[(int64_t)kb * p.sb_k];
   };
 
   f32x4 acc[MT][NT];
@@ -273,12 +675,10 @@ void fp8_tile_kernel(Fp8Gemm p) {
   const int frow = (lane & 15) * 128, fpiece = ((lane >> 4) ^ (lane & 7)) * 16;
   auto frag = [&](const char* base, int block) __attribute__((always_inline)) {
     const char* r = base + block * 2048 + frow;
-    return FragOf<WIDE>::of(join8(*(const u32x4*)(r + fpiece), *(const u32x4*)(r + (fpiece ^ 64))));
+    return widen(join8(*(const u32x4*)(r + fpiece), *(const u32x4*)(r + (fpiece ^ 64))));
   };
-  if (nkb > 0) {
-    scales(0);
-    issue(0, 0);
-  }
+  scales(0);
+  issue(0, 0);
   for (int kb = 0; kb < nkb; ++kb) {
     // this wave's loads of the stage have landed; behind the barrier everyone's have, and everyone
     // has read the stage that is loaded next
@@ -295,7 +695,7 @@ void fp8_tile_kernel(Fp8Gemm p) {
       const char* As = lds + (kb & 1) * STAGE + wm * WTM * 128;
       const char* Bs = lds + (kb & 1) * STAGE + BM * 128 + wn * WTN * 128;
       // one column block of MT MFMAs at a time, the multiply-adds of the block before in their shadow
-      typename FragOf<WIDE>::type fa[MT], fb[2];
+      Wide fa[MT], fb[2];
       f32x4 pr[2][MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) fa[i] = frag(As, i);
@@ -318,28 +718,7 @@ void fp8_tile_kernel(Fp8Gemm p) {
     }
   }
 
-  // ---- store
-  if (!(wm * WTM < mv && n_on)) return;
-  if (poison) {
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] = acc[i][j] + __builtin_nanf("");
-  }
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int m = wm * WTM + i * 16 + (lane & 15);
-    if (m >= mv) continue;
-#pragma unroll
-    for (int j = 0; j < NT; j += 2) {
-      const int n = wn * WTN + j * 16 + 8 * (lane >> 4);
-      if (n >= nv) continue;
-      if (MODE == GM_MATMUL && p.splits > 1)
-        store_row8<EL_F32>(d + ((int64_t)(m0 + m) * p.N + n0 + n) * 4, nv - n, acc[i][j], acc[i][j + 1]);
-      else
-        store_row8<OT>(d + ((int64_t)(m0 + m) * p.ldd + n0 + n) * elt_size(OT), nv - n, acc[i][j], acc[i][j + 1]);
-    }
-  }
+  if (active) store_tile<MODE, OT, false>(p, tile, wm * WTM, wn * WTN, acc);
 }
 
 // D = sum of the K ranges' parts, in their order
@@ -492,14 +871,29 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Gemm p) {
   }
 }
 
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN, bool WIDE>
-hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
+template <int MODE, int BM, int BN>
+int64_t count_tiles(Fp8Gemm& p) {
   p.tiles_n = (p.N + BN - 1) / BN;
   p.tiles_m = (p.M + BM - 1) / BM;
   if (MODE == GM_GROUPED) p.tiles_m += (p.experts < p.M ? p.experts : p.M) + 1;  // (at most)
-  const int64_t blocks = (int64_t)p.tiles_m * p.tiles_n * (MODE == GM_WGRAD ? p.experts : p.splits);
-  if (blocks >= 0x7fffffffLL / (64 * WGM * WGN)) return hipErrorInvalidConfiguration;
-  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, WIDE><<<(unsigned)blocks, 64 * WGM * WGN, 0, s>>>(p);
+  return (int64_t)p.tiles_m * p.tiles_n * (MODE == GM_WGRAD ? p.experts : p.splits);
+}
+
+// A workgroup for each compute unit (a multiple of 8: a workgroup's tiles are all of one XCD's share).
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
+hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
+  const int64_t tiles = count_tiles<MODE, BM, BN>(p);
+  if (tiles >= 0x7fffffffLL / 512) return hipErrorInvalidConfiguration;
+  const int whole = p.cus >= 8 ? p.cus & ~7 : 8;
+  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, S><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int MODE, int OT>
+hipError_t launch_wide(Fp8Gemm& p, hipStream_t s) {
+  const int64_t tiles = count_tiles<MODE, 128, 128>(p);
+  if (tiles >= 0x7fffffffLL / 512) return hipErrorInvalidConfiguration;
+  fp8_wide_kernel<MODE, OT, 128, 128, 2, 2><<<(unsigned)tiles, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -507,14 +901,16 @@ template <int MODE, int OT>
 hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
   if constexpr (OT != EL_F32) {
     if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
-      const hipError_t e = launch_tile<MODE, OT, 256, 256, 4, 2, false>(p, s);
+      const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
+      if (big < p.cus) return launch_tile<MODE, OT, 128, 128, 2, 2, 4>(p, s);
+      const hipError_t e = launch_tile<MODE, OT, 256, 256, 4, 2, 2>(p, s);
       if (e != hipSuccess || p.splits == 1) return e;
       const int64_t b = ((int64_t)p.M * p.N + 2047) / 2048;
       fp8_join_kernel<OT><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, s>>>(p);
       return hipGetLastError();
     }
   }
-  return launch_tile<MODE, OT, 128, 128, 2, 2, true>(p, s);
+  return launch_wide<MODE, OT>(p, s);
 }
 
 template <int MODE, int OT, int MT>

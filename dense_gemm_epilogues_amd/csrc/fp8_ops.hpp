@@ -30,6 +30,7 @@ struct Fp8Gemm {
   int tiles_m, tiles_n;
   int splits, kb_per_split;          // matmul: K ranges, each into its own part of `part`
   float* part;                       // [splits][M][N]
+  int cus;                           // of the device
 };
 
 enum GemmMode : int { GM_MATMUL = 0, GM_GROUPED = 1, GM_WGRAD = 2 };
