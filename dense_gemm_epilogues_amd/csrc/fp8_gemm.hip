@@ -113,6 +113,7 @@ __device__ __forceinline__ void store_row8(char* d, int n, f32x4 lo, f32x4 hi) {
 
 // ---------------------------------------------------------------------------------------- tiles
 constexpr int kGroupM = 8;
+constexpr int kTilesAtOnce = 512;
 
 template <class T>
 __device__ __forceinline__ T* global_ptr(T* p) {
@@ -304,6 +305,48 @@ __device__ __forceinline__ void store_tile(const Fp8Gemm& p, const Tile& t, int 
     for (int j = 0; j < NT; j += 2) {
       const int left = t.nv - n_at - n0 - j * 16;
       if (left > 0) store_row8<OT>(row + j * 16 * elt_size(OT), left, acc[i][j], acc[i][j + 1]);
+    }
+  }
+}
+
+// The same for 16-bit outputs and rows in row_in's order: neighbouring lanes, which hold neighbouring rows,
+// first trade halves of 64 columns, so that a store instruction writes whole 128-byte lines, which leave the
+// caches to the operands (non-temporal).  The experts' weight gradients, 2.7 GB of stores: 1518 us with half
+// lines, 1345 with whole ones, 1220 non-temporal.
+template <int MODE, int OT, int MT, int NT>
+__device__ __forceinline__ void store_lines(const Fp8Gemm& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
+  const int lane = here(lane_id());
+  const bool odd = lane & 1;
+  char* d = tile_d<MODE, OT>(p, t) + (m_at * p.ldd + n_at) * 2;
+  const int n0 = 8 * (lane >> 4) + (odd ? 32 : 0);
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = row_in(i, lane & 14);
+    char* row = d + (m * p.ldd + n0) * 2;
+    const int rows = t.mv - m_at - m;
+#pragma unroll
+    for (int j = 0; j < NT; j += 4) {
+      u32x4 a, b, x, y;  // the row's first and second 32 columns' pieces; traded
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        a[h] = pack2_elt<OT>(acc[i][j + h / 2][2 * (h & 1)], acc[i][j + h / 2][2 * (h & 1) + 1]);
+        b[h] = pack2_elt<OT>(acc[i][j + 2 + h / 2][2 * (h & 1)], acc[i][j + 2 + h / 2][2 * (h & 1) + 1]);
+        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
+        x[h] = odd ? got : a[h];
+        y[h] = odd ? b[h] : got;
+      }
+      const int left = t.nv - n_at - n0 - j * 16;
+      if (left >= 8) {
+        if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)(row + j * 32));
+        if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(row + p.ldd * 2 + j * 32));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e >= left) continue;
+          if (rows > 0) *(uint16_t*)(row + j * 32 + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+          if (rows > 1) *(uint16_t*)(row + p.ldd * 2 + j * 32 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+        }
+      }
     }
   }
 }
@@ -590,7 +633,8 @@ void fp8_tile_kernel(Fp8Gemm p) {
       // (the last loads write LDS too: not after the workgroup has left it)
       if (!more) __builtin_amdgcn_s_waitcnt(0x0070);
       add_last();
-      store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
+      if constexpr (OT == EL_F32) store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
+      else store_lines<MODE, OT>(args_here(), cur, wm * WTM, wn * WTN, acc);
       done = !more;
       clear();
       cur = ahead;
@@ -879,13 +923,13 @@ int64_t count_tiles(Fp8Gemm& p) {
   return (int64_t)p.tiles_m * p.tiles_n * (MODE == GM_WGRAD ? p.experts : p.splits);
 }
 
-// A workgroup for each compute unit (a multiple of 8: a workgroup's tiles are all of one XCD's share).
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
+// As many workgroups as run at once (a multiple of 8: a workgroup's tiles are all of one XCD's share).
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int PER_CU>
 hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
   const int64_t tiles = count_tiles<MODE, BM, BN>(p);
   if (tiles >= 0x7fffffffLL / 512) return hipErrorInvalidConfiguration;
-  const int whole = p.cus >= 8 ? p.cus & ~7 : 8;
-  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, S><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
+  const int whole = (p.cus >= 8 ? p.cus & ~7 : 8) * PER_CU;
+  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, 2><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -899,15 +943,27 @@ hipError_t launch_wide(Fp8Gemm& p, hipStream_t s) {
 
 template <int MODE, int OT>
 hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
-  if constexpr (OT != EL_F32) {
-    if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
-      const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
-      if (big < p.cus) return launch_tile<MODE, OT, 128, 128, 2, 2, 4>(p, s);
-      const hipError_t e = launch_tile<MODE, OT, 256, 256, 4, 2, 2>(p, s);
-      if (e != hipSuccess || p.splits == 1) return e;
+  if constexpr (MODE == GM_MATMUL) {
+    if (p.splits > 1) {
+      Fp8Gemm q = p;
+      q.d = p.part;
+      q.ldd = p.N;
+      const hipError_t e = OT == EL_F32 ? launch_wide<MODE, EL_F32>(q, s) : launch_tile<MODE, EL_F32, 128, 128, 2, 2, 2>(q, s);
+      if (e != hipSuccess) return e;
       const int64_t b = ((int64_t)p.M * p.N + 2047) / 2048;
       fp8_join_kernel<OT><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, s>>>(p);
       return hipGetLastError();
+    }
+  }
+  if constexpr (OT != EL_F32) {
+    if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
+      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 41 us,
+      // 62 with 80 large tiles); with more the large ones, which read half as much through the caches
+      // (8192 x 17408 x 5120: 711 us, 849 with small ones)
+      const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
+      // so with few rows an expert: 64 experts of 64 rows, n 4096, k 5120: 255 us, 273 with large tiles (of 128: 355, 287)
+      if (big < p.cus || (MODE == GM_GROUPED && p.M <= 96 * (int64_t)p.experts)) return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(p, s);
+      return launch_tile<MODE, OT, 256, 256, 4, 2, 1>(p, s);
     }
   }
   return launch_wide<MODE, OT>(p, s);
@@ -931,7 +987,25 @@ hipError_t launch_rows(Fp8Gemm& p, int rows_at_once, hipStream_t s) {
 
 }  // namespace
 
-int fp8_splits(int m, int n, int k) { return 1; }
+// K ranges of a product with few tiles.  A step of 128 x 128 tiles takes 0.6 us with two of them on every compute
+// unit; ranges cost a launch (5 us) and their parts' way through memory, written and read at about 4 TB/s.  By
+// this model 64 x 5120 x 5120 takes 5 ranges (19 us, unsplit 27), 128 x 5120 x 17408 takes 10 (84 us unsplit),
+// 1024 x 4096 x 5120 none (30 us, 37 with 2).
+int fp8_splits(int m, int n, int k) {
+  const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 127) / 128);
+  const int blocks = (k + kScaleBlock - 1) / kScaleBlock;
+  int best = 1;
+  double least = blocks * 0.6;
+  for (int s = 2; s * tiles <= kTilesAtOnce && s <= blocks / 4; ++s) {
+    const int each = (blocks + s - 1) / s, parts = (blocks + each - 1) / each;
+    const double us = each * 0.6 + 5.0 + 8.0 * parts * m * n / 4e6;
+    if (us < least) {
+      least = us;
+      best = parts;
+    }
+  }
+  return best;
+}
 
 hipError_t launch_fp8_tiles(int mode, int out, Fp8Gemm& p, hipStream_t s) {
 #define EP_CASE(M_, O_) \
