@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "ep.h"
+#include "api_shared.hpp"
 #include "ep_internal.hpp"
 #include "static_scratch.hpp"
 

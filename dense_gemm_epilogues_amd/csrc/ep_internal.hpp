@@ -100,12 +100,6 @@ GemmLauncher gemm_partial_launcher(int dtype, int layout, bool dual, int cfg);
 GemmLauncher gemm_fixup_launcher(int dtype, int epi, int cfg);
 const char* gemm_kernel_name(int dtype, int layout, int epi, int cfg);
 
-// ---- shared by the files of the C ABI (ep_api.cpp): the thread's last error, and the check that a
-// stream belongs to the calling thread's current device, which is a gfx950 (and its number of compute units)
-int api_fail(int status, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-void api_clear();
-int api_stream(void* stream, int* cus = nullptr);
-
 // ---- unfused baseline and reduction kernels (elementwise.hip)
 hipError_t launch_bias_add(int dtype, void* z, int64_t ldz, const void* bias, int M, int N, hipStream_t s);
 hipError_t launch_relu_pack(int dtype, const void* z, int64_t ldz, void* y, int64_t ldy, uint32_t* aux,

@@ -1,7 +1,7 @@
 // C ABI of the 8-bit block-scaled products and the expert operators: validation and dispatch.  Every
 // call only enqueues kernels; workspaces are the caller's.
 #include "ep.h"
-#include "ep_internal.hpp"
+#include "api_shared.hpp"
 #include "fp8_ops.hpp"
 
 using namespace ep;
