@@ -62,12 +62,24 @@ __device__ __forceinline__ void load_tail(const char* p, int n, float* f) {
   }
 }
 
+// 16 bytes from and to p; NT: past the caches' replacement (non-temporal)
+template <bool NT>
+__device__ __forceinline__ u32x4 get16(const char* p) {
+  if constexpr (NT) return __builtin_nontemporal_load((const u32x4_u*)p);
+  else return *(const u32x4_u*)p;
+}
+template <bool NT>
+__device__ __forceinline__ void put16(char* p, u32x4 w) {
+  if constexpr (NT) __builtin_nontemporal_store(w, (u32x4_u*)p);
+  else *(u32x4_u*)p = w;
+}
+
 // 8 elements from p, those at or past `n` as zeros
-template <int E>
+template <int E, bool NT = false>
 __device__ __forceinline__ void load8(const char* p, int n, float* f) {
   if constexpr (E == EL_F32) {
     if (n >= 8) {
-      const u32x4 a = *(const u32x4_u*)p, b = *(const u32x4_u*)(p + 16);
+      const u32x4 a = get16<NT>(p), b = get16<NT>(p + 16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[i] = elt_f32<E>(a[i]);
@@ -78,7 +90,7 @@ __device__ __forceinline__ void load8(const char* p, int n, float* f) {
     }
   } else {
     if (n >= 8) {
-      const u32x4 a = *(const u32x4_u*)p;
+      const u32x4 a = get16<NT>(p);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f[2 * i] = elt_f32<E>(a[i] & 0xffffu);
@@ -91,12 +103,12 @@ __device__ __forceinline__ void load8(const char* p, int n, float* f) {
 }
 
 // 8 elements to p, those at or past `n` left alone
-template <int E>
+template <int E, bool NT = false>
 __device__ __forceinline__ void store8(char* p, int n, const float* f) {
   if constexpr (E == EL_F32) {
     if (n >= 8) {
-      *(u32x4_u*)p = __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]});
-      *(u32x4_u*)(p + 16) = __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]});
+      put16<NT>(p, __builtin_bit_cast(u32x4, f32x4{f[0], f[1], f[2], f[3]}));
+      put16<NT>(p + 16, __builtin_bit_cast(u32x4, f32x4{f[4], f[5], f[6], f[7]}));
       return;
     }
   } else {
@@ -104,7 +116,7 @@ __device__ __forceinline__ void store8(char* p, int n, const float* f) {
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = pack2_elt<E>(f[2 * i], f[2 * i + 1]);
-      *(u32x4_u*)p = w;
+      put16<NT>(p, w);
       return;
     }
   }

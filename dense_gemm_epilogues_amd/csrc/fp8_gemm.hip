@@ -798,8 +798,9 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm p) {
 // deal out the scale blocks, stream them from memory into registers and join their sums in LDS.
 // Rows of a come from the caches, MT x 16 at a time.
 template <int MODE, int OT, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Gemm p) {
-  constexpr int U = MT == 1 ? 4 : 2;  // scale blocks in flight per wave
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(MT > 1 ? 2 : MODE == GM_GROUPED ? 3 : 4)))
+void fp8_rows_kernel(Fp8Gemm p) {
+  constexpr int U = 2;  // scale blocks in flight per wave, twice
   __shared__ f32x4 red[NW][MT][64];
   const int lane = lane_id(), wave = wave_id();
   const int n0 = (int)blockIdx.x * 16;
@@ -812,17 +813,14 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Gemm p) {
     for (int e0 = 0; e0 < p.experts && found < 0; e0 += 64) {
       int q0 = 0, q1 = 0;
       if (e0 + lane < p.experts) group_rows(p.offsets, e0 + lane, p.M, q0, q1);
-      const int c = wave_scan(q1 > q0 ? 1 : 0);
-      const uint64_t hit = __ballot(q1 > q0 && seen + c == (int)blockIdx.y + 1);
-      if (hit) {
-        const int l = __builtin_ctzll(hit);
-        found = e0 + l;
-        r0 = __shfl(q0, l);
-        r1 = __shfl(q1, l);
+      uint64_t some = __ballot(q1 > q0);
+      const int n = __builtin_popcountll(some), skip = (int)blockIdx.y - seen;
+      if (skip < n) {
+        for (int k = 0; k < skip; ++k) some &= some - 1;
+        found = e0 + __builtin_ctzll(some);
       }
-      seen += __shfl(c, 63);
+      seen += n;
     }
-    found = __builtin_amdgcn_readfirstlane(found);
     if (found < 0) {
       if (seen != (int)blockIdx.y) return;
       r0 = clampi(p.offsets[p.experts], 0, p.M);
@@ -832,6 +830,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_rows_kernel(Fp8Gemm p) {
       }
       return;
     }
+    group_rows(p.offsets, found, p.M, r0, r1);
     r0 = __builtin_amdgcn_readfirstlane(r0);
     r1 = __builtin_amdgcn_readfirstlane(r1);
     b += (int64_t)found * p.b_e;

@@ -26,7 +26,7 @@ __device__ __forceinline__ u32x4 quant16(const float* f, float inv) {
   return w;
 }
 
-__device__ __forceinline__ void put16(uint8_t* q, int n, u32x4 w) {
+__device__ __forceinline__ void put_bytes(uint8_t* q, int n, u32x4 w) {
   if (n >= 16) {
     *(u32x4_u*)q = w;
   } else {
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(QuantArgs p, in
   for (int d = 1; d < 8; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d));
   if (!on) return;
   const u32x4 w = quant16(f, scale_inv(amax));
-  if (n > 0) put16(p.q + row * p.ldq + col, n, w);
+  if (n > 0) put_bytes(p.q + row * p.ldq + col, n, w);
   if (sub == 0) p.scale[(int64_t)kb * p.m + row] = scale_of(amax);
 }
 
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs p, in
       const int pos = (sub * 4) ^ (((r >> 4) & 3) << 3);
       *(u32x4*)(tile + r * kScaleBlock + pos * 4) = w;
     } else if (m0 + r < p.m && col < p.k) {
-      put16(p.q + (int64_t)(m0 + r) * p.ldq + col, p.k - col, w);
+      put_bytes(p.q + (int64_t)(m0 + r) * p.ldq + col, p.k - col, w);
     }
   }
   if constexpr (TRANS) {
@@ -169,7 +169,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs p, in
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const int k = k0 + 4 * kd + b;
-        if (k < p.k) put16(p.q + (int64_t)k * p.ldq + mm, p.m - mm, out[b]);
+        if (k < p.k) put_bytes(p.q + (int64_t)k * p.ldq + mm, p.m - mm, out[b]);
       }
     }
   }
