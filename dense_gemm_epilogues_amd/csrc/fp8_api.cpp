@@ -50,9 +50,11 @@ ep_status check_product(int64_t rows_a, int64_t rows_b, int64_t k, const void* a
   return EP_OK;
 }
 
-// workgroups that few-row products take; the same rule in ep_matmul_fp8 and the grouped product
-constexpr int64_t kRowsPath = 32;        // rows of a matmul
-constexpr int64_t kRowsPerExpert = 16;   // mean rows of an expert
+// Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 20 us; 16 rows in
+// tiles with K ranges 26) and up to 4 rows an expert on average (64 experts, n 4096, k 5120: 32 rows in 90 us, 109 in
+// tiles, 256 rows in 220 and 229, 384 rows even).
+constexpr int64_t kRowsPath = 8;
+bool few_rows(int64_t rows, int64_t experts) { return rows <= 4 * experts; }
 
 }  // namespace
 
@@ -111,7 +113,7 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
     }
   }
   if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
-  if (rows) return done(launch_fp8_rows(GM_MATMUL, out, p, m <= 16 ? 16 : 32, (hipStream_t)stream), "matmul_fp8");
+  if (rows) return done(launch_fp8_rows(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
   return done(launch_fp8_tiles(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
 }
 
@@ -135,8 +137,8 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
   p.offsets = offsets; p.experts = (int)experts;
   p.M = (int)rows; p.N = (int)n; p.K = (int)k;
   p.splits = 1;
-  if (rows <= kRowsPerExpert * experts)
-    return done(launch_fp8_rows(GM_GROUPED, out, p, rows <= 4 * experts ? 16 : 32, (hipStream_t)stream), "grouped_matmul_fp8");
+  if (few_rows(rows, experts))
+    return done(launch_fp8_rows(GM_GROUPED, out, p, (hipStream_t)stream), "grouped_matmul_fp8");
   return done(launch_fp8_tiles(GM_GROUPED, out, p, (hipStream_t)stream), "grouped_matmul_fp8");
 }
 

@@ -36,8 +36,8 @@ struct Fp8Gemm {
 enum GemmMode : int { GM_MATMUL = 0, GM_GROUPED = 1, GM_WGRAD = 2 };
 
 hipError_t launch_fp8_tiles(int mode, int out, Fp8Gemm& p, hipStream_t s);
-// few rows: weights stream straight into registers; max_rows: rows a workgroup takes at a time (16, 32, 64)
-hipError_t launch_fp8_rows(int mode, int out, Fp8Gemm& p, int rows_at_once, hipStream_t s);
+// few rows: b streams past them
+hipError_t launch_fp8_rows(int mode, int out, Fp8Gemm& p, hipStream_t s);
 int fp8_splits(int m, int n, int k);
 
 struct QuantArgs {
