@@ -154,3 +154,27 @@ def test_expert_abi():
     back = lambda **kw: L.ep_expert_combine_backward(*{**dict(g=P, t=4, h=8, ldg=8, elt=1, y=P, rows=8, ldy=8, pos=P, k=2, src=P, w=P, ldw=2, dy=P, lddy=8, dw=P, st=None), **kw}.values())  # noqa: E731
     for kw, want in (({"g": None}, INVALID), ({"dw": None}, INVALID), ({"dy": None}, INVALID), ({"lddy": 4}, INVALID), ({"elt": -1}, UNSUPPORTED)):
         assert back(**kw) == want, kw
+
+
+def test_matmul_workspace():
+    """K ranges of a product with few tiles need the workspace that is asked for."""
+    L = ep.lib()
+    need = ctypes.c_size_t(7)
+    assert L.ep_matmul_fp8_workspace(8192, 8192, 4096, ctypes.byref(need)) == 0 and need.value == 0
+    assert L.ep_matmul_fp8_workspace(8, 512, 8192, ctypes.byref(need)) == 0 and need.value == 0
+    assert L.ep_matmul_fp8_workspace(128, 512, 8192, ctypes.byref(need)) == 0
+    parts, rest = divmod(need.value, 128 * 512 * 4)
+    assert rest == 0 and 2 <= parts <= 64 // 4
+    args = lambda ws, size: (128, 512, 8192, P, 8192, P, 1, 128, P, 8192, P, 64, 1, P, 512, 1, ws, size, None)  # noqa: E731
+    for ws, size in ((None, 0), (None, need.value), (P, need.value - 1), (P + 8, need.value)):
+        assert L.ep_matmul_fp8(*args(ws, size)) == INVALID
+    assert b"workspace" in L.ep_last_error()
+
+
+def test_scale_stride_limits():
+    L = ep.lib()
+    ok = [64, 64, 256, P, 256, P, 1, 64, P, 256, P, 2, 1, P, 64, 1, None, 0, None]
+    for at, value in ((6, 1 << 21), (11, 1 << 29)):
+        args = list(ok)
+        args[at] = value
+        assert L.ep_matmul_fp8(*args) == UNSUPPORTED
