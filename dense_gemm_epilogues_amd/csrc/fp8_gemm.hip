@@ -15,8 +15,8 @@
 // Next to a bf16 or fp16 output's rounding (1.7e-3, 2.1e-4 of the norm) that is nothing, and it is the
 // unit's only way to its full rate.  Where it would show or buys nothing the operands are widened to
 // fp16 first, which holds every e4m3 value, and multiplied by v_mfma_f32_16x16x32_f16, whose sums are
-// fp32 throughout (WIDE): fp32 outputs, sums of at most 256 values (bound by the output's bytes), and
-// the few-row kernel (bound by the weights').
+// fp32 throughout (fp8_wide_kernel): fp32 outputs, sums of at most 256 values (bound by the output's
+// bytes), and the few-row kernel (bound by the weights').
 #include "fp8_device.hpp"
 
 namespace ep {
@@ -382,10 +382,15 @@ __device__ constexpr bool read_first(int j) {
 // Two barriers a step.  Behind the first, after the first column block, every wave holds its fragments of a:
 // the stage's part of a is free, and the loads of the step S ahead go into it.  Behind the second, before the
 // last two blocks, every wave holds what it reads of b as well: the loads of b follow, and the next stage has
-// landed.  So the loads, which take half of the step's time in the address unit, are spread over it.  The last two
-// blocks' MFMAs go row block by row block, each row block's fragment of a followed by the next step's, so the
-// matrix unit does not wait for a step's first reads.  The steps run on from tile to tile: the next tile's
-// operands land while this one's last steps are multiplied.
+// landed.  The last two blocks' MFMAs go row block by row block, each row block's fragment of a followed by the
+// next step's, and a step's last product is added behind the next step's first MFMA, so that the matrix unit
+// waits little between steps.  The steps run on from tile to tile: the next tile's operands land while this
+// one's last steps are multiplied.
+//
+// Measured on one MI355X: 8192 x 17408 x 5120 in 611 us, 2389 TFLOP/s (one tile a workgroup, all loads at a step's
+// start: 667).  What bounds it is power: the card runs it at 1.7 GHz of 2.4, the matrix unit is busy for 60 % of
+// the cycles.  From registers alone the same MFMAs with random operands reach 3863 TFLOP/s, 3484 with their
+// multiply-adds; without the loads (operands left in LDS) a step takes 12 % fewer cycles, without the multiply-adds 15 %.
 template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
 void fp8_tile_kernel(Fp8Gemm p) {

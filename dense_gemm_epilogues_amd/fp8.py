@@ -70,7 +70,9 @@ def _contracted(k):
 @streamed
 def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
     """(a a_scale) (b b_scale)^T: a (M x K) with scales (M, ceil(K / 128)), b (N x K) with scales
-    (ceil(N / 128), ceil(K / 128)); K a multiple of 16.  Summed in fp32, rounded once to out_dtype."""
+    (ceil(N / 128), ceil(K / 128)); K a multiple of 16.  Summed in fp32, rounded once to out_dtype.  (16-bit
+    outputs: products of 8 neighbouring K are added in fixed point first, about 1.5e-5 of the result's norm off;
+    float32 outputs are summed in fp32 throughout, at half the rate.)"""
     check("a", a, E4M3, (None, None))
     m, k = a.shape
     check("b", b, E4M3, (None, k), a.device)
