@@ -33,11 +33,17 @@ def check(name, t, dtypes, shape, device=None):
     (None: any size) on `device`."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if t.dtype is not dtypes and (isinstance(dtypes, torch.dtype) or t.dtype not in dtypes):
+    dtype = t.dtype
+    if dtype is not dtypes and (isinstance(dtypes, torch.dtype) or dtype not in dtypes):
         want = dtypes if isinstance(dtypes, torch.dtype) else " or ".join(str(d) for d in dtypes)
-        raise ValueError(f"{name} must be {want}, got {t.dtype}")
+        raise ValueError(f"{name} must be {want}, got {dtype}")
     s = t.shape
-    if len(s) != len(shape) or any(w is not None and w != g for w, g in zip(shape, s)):
+    fits = len(s) == len(shape)
+    if fits:
+        for w, g in zip(shape, s):
+            if w is not None and w != g:
+                fits = False
+    if not fits:
         want = tuple("any" if w is None else w for w in shape)
         raise ValueError(f"{name} must have shape {want}, got {tuple(s)}")
     if device is not None and t.device != device:
@@ -46,10 +52,10 @@ def check(name, t, dtypes, shape, device=None):
 
 def unit_columns(name, t):
     """Row stride of a matrix whose rows are contiguous and apart (ValueError otherwise)."""
-    rows, cols = t.shape[-2], t.shape[-1]
-    if t.stride(-1) != 1 and cols > 1:
+    rows, cols = t.shape[-2:]
+    ld, step = t.stride()[-2:]
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride, got stride {t.stride()}")
-    ld = t.stride(-2)
     if rows <= 1:
         return max(ld, cols)
     if ld < cols:
@@ -63,7 +69,7 @@ def contiguous(name, t):
 
 
 def on_device(t):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"operands must be on a CUDA (HIP) device, got {t.device}")
 
 
@@ -92,13 +98,12 @@ def streamed(f):
         if stream is not None:
             with torch.cuda.stream(stream):
                 return f(first, *args, **kw)
-        t = first if isinstance(first, torch.Tensor) else None
-        if t is not None and t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
+        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
                 return f(first, *args, **kw)
         return f(first, *args, **kw)
     return call
 
 
 def current_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())

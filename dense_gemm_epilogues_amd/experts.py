@@ -11,6 +11,7 @@ Every function only enqueues kernels (libep.so, `ep_expert_*` in include/ep.h) o
 or on `stream`.
 """
 import ctypes
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -30,6 +31,14 @@ class ExpertOrder(NamedTuple):
     offsets: torch.Tensor
 
 
+@lru_cache(maxsize=256)
+def _order_sizes(slots, experts, align):
+    """(capacity, workspace bytes): whole numbers that depend on these alone."""
+    capacity, need = ctypes.c_int64(), ctypes.c_size_t()
+    _check(lib().ep_expert_order_sizes(slots, experts, align, ctypes.byref(capacity), ctypes.byref(need)))
+    return capacity.value, need.value
+
+
 @streamed
 def expert_order(ids, experts, align=1):
     """The ExpertOrder of ids (T, k; int32 or int64, contiguous): slots sorted by expert, in (token, choice)
@@ -40,16 +49,14 @@ def expert_order(ids, experts, align=1):
     contiguous("ids", ids)
     on_device(ids)
     t, k = ids.shape
-    L = lib()
-    cap, need = ctypes.c_int64(), ctypes.c_size_t()
-    _check(L.ep_expert_order_sizes(t * k, experts, align, ctypes.byref(cap), ctypes.byref(need)))
-    pos = torch.empty((t, k), dtype=torch.int32, device=ids.device)
-    src = torch.empty((cap.value,), dtype=torch.int32, device=ids.device)
-    offsets = torch.empty((experts + 1,), dtype=torch.int32, device=ids.device)
-    ws = torch.empty((need.value,), dtype=torch.uint8, device=ids.device) if need.value else None
-    _check(L.ep_expert_order(ids.data_ptr(), ids.element_size(), t * k, experts, align, pos.data_ptr(), src.data_ptr(),
-                             offsets.data_ptr(), ws.data_ptr() if ws is not None else None, need.value,
-                             current_stream(ids)))
+    capacity, need = _order_sizes(t * k, experts, align)
+    dev = ids.device
+    pos = torch.empty((t, k), dtype=torch.int32, device=dev)
+    src = torch.empty((capacity,), dtype=torch.int32, device=dev)
+    offsets = torch.empty((experts + 1,), dtype=torch.int32, device=dev)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dev) if need else None
+    _check(lib().ep_expert_order(ids.data_ptr(), ids.element_size(), t * k, experts, align, pos.data_ptr(), src.data_ptr(),
+                                 offsets.data_ptr(), ws.data_ptr() if need else None, need, current_stream(ids)))
     return ExpertOrder(pos, src, offsets)
 
 

@@ -11,6 +11,7 @@ Every function only enqueues kernels (libep.so, `ep_*_fp8` in include/ep.h) on t
 on `stream`.
 """
 import ctypes
+from functools import lru_cache
 
 import torch
 
@@ -67,6 +68,14 @@ def _contracted(k):
         raise ValueError(f"the contracted length must be a multiple of 16, got {k}")
 
 
+@lru_cache(maxsize=256)
+def _workspace(m, n, k):
+    """Bytes of a product's workspace, which depend on its sizes alone."""
+    need = ctypes.c_size_t()
+    _check(lib().ep_matmul_fp8_workspace(m, n, k, ctypes.byref(need)))
+    return need.value
+
+
 @streamed
 def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
     """(a a_scale) (b b_scale)^T: a (M x K) with scales (M, ceil(K / 128)), b (N x K) with scales
@@ -87,13 +96,11 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
         return out
     if not k:
         return out.zero_()
-    L = lib()
-    need = ctypes.c_size_t()
-    _check(L.ep_matmul_fp8_workspace(m, n, k, ctypes.byref(need)))
-    ws = torch.empty(need.value, dtype=torch.uint8, device=a.device) if need.value else None
-    _check(L.ep_matmul_fp8(m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb,
+    need = _workspace(m, n, k)
+    ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
+    _check(lib().ep_matmul_fp8(m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb,
                            b_scale.data_ptr(), *b_scale.stride(), out.data_ptr(), ldd, ELT[out_dtype],
-                           ws.data_ptr() if ws is not None else None, need.value, current_stream(a)))
+                           ws.data_ptr() if need else None, need, current_stream(a)))
     return out
 
 
