@@ -951,7 +951,7 @@ hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
   }
   if constexpr (OT != EL_F32) {
     if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
-      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 41 us,
+      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 35 us,
       // 62 with 80 large tiles); with more the large ones, which read half as much through the caches
       // (8192 x 17408 x 5120: 711 us, 849 with small ones)
       const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
