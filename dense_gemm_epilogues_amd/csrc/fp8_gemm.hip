@@ -77,12 +77,6 @@ __device__ __forceinline__ int xcd_order(int bid, int n) {
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return min(max(v, lo), hi); }
 
-// rows of group e, kept inside [0, rows] whatever the offsets hold
-__device__ __forceinline__ void group_rows(const int* offsets, int e, int rows, int& r0, int& r1) {
-  r0 = clampi(offsets[e], 0, rows);
-  r1 = clampi(offsets[e + 1], r0, rows);
-}
-
 // v, computed here and not kept in registers from before the loop around it
 __device__ __forceinline__ int here(int v) {
   asm volatile("" : "+v"(v));
@@ -103,6 +97,33 @@ __device__ __forceinline__ int wave_scan(int v) {  // inclusive sum over the lan
     if (lane >= d) v += u;
   }
   return v;
+}
+
+__device__ __forceinline__ int wave_max_scan(int v) {  // inclusive maximum over the lanes
+  const int lane = here(lane_id());
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v = max(v, u);
+  }
+  return v;
+}
+
+// Rows of the 64 groups from e0 on, one a lane (past the last group: none), kept inside [0, rows] and apart
+// from each other whatever the offsets hold: one below an earlier one counts as that one.  So there are never
+// more tiles than the launch counted on, which the walk over the tiles needs, and no row has two groups.
+// `top` is the greatest offset before group e0, and afterwards before group e0 + 64.
+__device__ __forceinline__ void groups_at(const int* offsets, int experts, int e0, int rows, int& top, int& r0, int& r1) {
+  const int e = e0 + lane_id();
+  r0 = r1 = 0;
+  if (e < experts) {
+    r0 = clampi(offsets[e], 0, rows);
+    r1 = clampi(offsets[e + 1], 0, rows);
+  }
+  if (__ballot(e < experts && r1 < r0)) r0 = wave_max_scan(r0);
+  r0 = max(r0, top);
+  r1 = max(r0, r1);
+  top = __builtin_amdgcn_readfirstlane(__shfl(r1, min(63, experts - 1 - e0)));
 }
 
 template <int OT>
@@ -154,16 +175,17 @@ struct Tile {
 template <int MODE, int BM, int BN>
 struct Tiles {
   int count;               // tiles there are
-  int e0 = 0, base = 0;    // grouped: a group to go on from, tile rows before it
+  int e0 = 0, base = 0, top = 0;  // grouped: a group to go on from, tile rows and the greatest offset before it
 
   __device__ __forceinline__ explicit Tiles(const Fp8Gemm& p) {
     if constexpr (MODE == GM_GROUPED) {
-      int total = (p.M - clampi(p.offsets[p.experts], 0, p.M) + BM - 1) / BM;
+      int total = 0, end = 0;
       for (int e = 0; e < p.experts; e += 64) {
-        int r0 = 0, r1 = 0;
-        if (e + lane_id() < p.experts) group_rows(p.offsets, e + lane_id(), p.M, r0, r1);
+        int r0, r1;
+        groups_at(p.offsets, p.experts, e, p.M, end, r0, r1);
         total += __shfl(wave_scan((r1 - r0 + BM - 1) / BM), 63);
       }
+      total += (p.M - end + BM - 1) / BM;
       count = __builtin_amdgcn_readfirstlane(total) * p.tiles_n;
     } else {
       count = p.tiles_m * p.tiles_n * (MODE == GM_WGRAD ? p.experts : p.splits);
@@ -195,8 +217,8 @@ struct Tiles {
     } else if constexpr (MODE == GM_GROUPED) {
       int e = -1, first = 0, r0 = 0, r1 = 0;
       for (; e0 < p.experts; e0 += 64) {
-        int q0 = 0, q1 = 0;
-        if (e0 + lane_id() < p.experts) group_rows(p.offsets, e0 + lane_id(), p.M, q0, q1);
+        int q0, q1, end = top;
+        groups_at(p.offsets, p.experts, e0, p.M, end, q0, q1);
         const int c = (q1 - q0 + BM - 1) / BM;
         const int ends = base + wave_scan(c);
         const uint64_t past = __ballot(ends * p.tiles_n > u);
@@ -209,11 +231,12 @@ struct Tiles {
           break;
         }
         base = __builtin_amdgcn_readfirstlane(__shfl(ends, 63));
+        top = end;
       }
       if (e < 0) {
         e = p.experts;
         first = base;
-        r0 = clampi(p.offsets[e], 0, p.M);
+        r0 = top;
         r1 = p.M;
       }
       t.part = __builtin_amdgcn_readfirstlane(e);
@@ -230,10 +253,8 @@ struct Tiles {
       place(p.tiles_n, u - t.part * tiles, p.tiles_m, tm, tn);
       t.m0 = tm * BM;
       t.mv = min(BM, p.M - t.m0);
-      int r0, r1;
-      group_rows(p.offsets, t.part, p.K, r0, r1);
-      r0 = __builtin_amdgcn_readfirstlane(r0);
-      r1 = __builtin_amdgcn_readfirstlane(r1);
+      const int r0 = __builtin_amdgcn_readfirstlane(clampi(p.offsets[t.part], 0, p.K));
+      const int r1 = __builtin_amdgcn_readfirstlane(clampi(p.offsets[t.part + 1], r0, p.K));
       t.kb0 = r0 / kScaleBlock;
       t.nkb = r1 / kScaleBlock - t.kb0;
       t.klen = r1;
@@ -816,30 +837,30 @@ __global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Fp8Gemm p) {
   int r0, r1;
   if constexpr (MODE == GM_GROUPED) {
     // the blockIdx.y-th group that has rows; behind the last one the rows that no group has
-    int seen = 0, found = -1;
+    int seen = 0, found = -1, top = 0;
     for (int e0 = 0; e0 < p.experts && found < 0; e0 += 64) {
-      int q0 = 0, q1 = 0;
-      if (e0 + lane < p.experts) group_rows(p.offsets, e0 + lane, p.M, q0, q1);
+      int q0, q1;
+      groups_at(p.offsets, p.experts, e0, p.M, top, q0, q1);
       uint64_t some = __ballot(q1 > q0);
       const int n = __builtin_popcountll(some), skip = (int)blockIdx.y - seen;
       if (skip < n) {
         for (int k = 0; k < skip; ++k) some &= some - 1;
-        found = e0 + __builtin_ctzll(some);
+        const int l = __builtin_ctzll(some);
+        found = e0 + l;
+        r0 = __builtin_amdgcn_readfirstlane(__shfl(q0, l));
+        r1 = __builtin_amdgcn_readfirstlane(__shfl(q1, l));
       }
       seen += n;
     }
     if (found < 0) {
       if (seen != (int)blockIdx.y) return;
-      r0 = clampi(p.offsets[p.experts], 0, p.M);
+      r0 = top;
       for (int i = threadIdx.x; i < (p.M - r0) * 16; i += 64 * NW) {
         const int n = n0 + (i & 15);
         if (n < p.N) store_elt<OT>((char*)p.d + ((int64_t)(r0 + (i >> 4)) * p.ldd + n) * elt_size(OT), 0.0f);
       }
       return;
     }
-    group_rows(p.offsets, found, p.M, r0, r1);
-    r0 = __builtin_amdgcn_readfirstlane(r0);
-    r1 = __builtin_amdgcn_readfirstlane(r1);
     b += (int64_t)found * p.b_e;
     sb += (int64_t)found * p.sb_e;
   } else {

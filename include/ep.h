@@ -315,7 +315,8 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
 
 /* ep_grouped_matmul_fp8: the same for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of a
  * (rows x k) times expert e's b (n x k at b + e * b_e, its scales at sb + e * sb_e).  offsets: experts + 1
- * whole numbers on the device, ascending from 0; rows from offsets[experts] on become zeros. */
+ * whole numbers on the device, ascending from 0; rows from offsets[experts] on become zeros.  (An offset outside
+ * 0 .. rows counts as the nearer end, one below an earlier one as that one; rows before offsets[0] are left alone.) */
 ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t experts, const int32_t* offsets, const void* a,
                                 int64_t lda, const float* sa, int64_t sa_m, int64_t sa_k, const void* b, int64_t b_e,
                                 int64_t ldb, const float* sb, int64_t sb_e, int64_t sb_n, int64_t sb_k, void* d, int64_t ldd,
