@@ -1,5 +1,6 @@
 """What the 8-bit and expert operators share: the C ABI's signatures, argument checks, streams."""
 import ctypes
+import inspect
 from functools import wraps
 
 import torch
@@ -93,15 +94,21 @@ def check_out(out, dtype, shape, device, inputs):
 def streamed(f):
     """Adds `stream=None`: with a torch stream, the call's kernels and the tensors it allocates go to
     that stream.  The launches run with the first tensor's device current."""
+    sig = inspect.signature(f)
+    params = list(sig.parameters.values())
+    name = params[0].name
+
     @wraps(f)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
         if stream is not None:
             with torch.cuda.stream(stream):
-                return f(first, *args, **kw)
+                return f(*args, **kw)
+        first = args[0] if args else kw.get(name)
         if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
             with torch.cuda.device(first.device):
-                return f(first, *args, **kw)
-        return f(first, *args, **kw)
+                return f(*args, **kw)
+        return f(*args, **kw)
+    call.__signature__ = sig.replace(parameters=params + [inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
