@@ -93,18 +93,22 @@ def check_out(out, dtype, shape, device, inputs):
 
 def streamed(f):
     """Adds `stream=None`: with a torch stream, the call's kernels and the tensors it allocates go to
-    that stream.  The launches run with the first tensor's device current."""
+    that stream, which must be on the first tensor's device.  The launches run with that device current."""
     sig = inspect.signature(f)
     params = list(sig.parameters.values())
     name = params[0].name
 
     @wraps(f)
     def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            return f(*args, **kw)  # (which refuses it)
         if stream is not None:
+            if stream.device != first.device:
+                raise ValueError(f"the stream is on {stream.device}, {name} is on {first.device}")
             with torch.cuda.stream(stream):
                 return f(*args, **kw)
-        first = args[0] if args else kw.get(name)
-        if isinstance(first, torch.Tensor) and first.is_cuda and first.get_device() != torch.cuda.current_device():
+        if first.get_device() != torch.cuda.current_device():
             with torch.cuda.device(first.device):
                 return f(*args, **kw)
         return f(*args, **kw)

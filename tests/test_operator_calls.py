@@ -1,8 +1,10 @@
 """How the 8-bit and expert operators can be called (CPU): every argument by its name, `stream` among them."""
 import inspect
+from types import SimpleNamespace
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
 
 import dense_gemm_epilogues_amd as ep
 
@@ -47,3 +49,13 @@ def test_signature_names_the_stream(f):
     params = inspect.signature(f).parameters
     assert [n for n in params if n in calls()[f]] == list(calls()[f])
     assert params["stream"].kind is inspect.Parameter.KEYWORD_ONLY and params["stream"].default is None
+
+
+@pytest.mark.parametrize("f", calls(), ids=lambda f: f.__name__)
+def test_stream_of_another_device_is_refused(f):
+    """Work on it would run on the wrong GPU, and unordered with the operands' stream."""
+    with FakeTensorMode(allow_non_fake_inputs=True):  # (tensors of device 0 without a GPU)
+        first, *rest = calls()[f].items()
+        on_gpu = torch.empty(first[1].shape, dtype=first[1].dtype, device="cuda:0")
+        with pytest.raises(ValueError, match="the stream is on cuda:1"):
+            f(**{first[0]: on_gpu}, **dict(rest), stream=SimpleNamespace(device=torch.device("cuda", 1)))
