@@ -42,7 +42,8 @@ ep_status check_product(int64_t rows_a, int64_t rows_b, int64_t k, const void* a
   EP_REQUIRE(aligned(sa, 4) && aligned(sb, 4), EP_ERR_INVALID_ARG, "scales must be 4-byte aligned");
   EP_REQUIRE(sa_m >= 0 && sa_k >= 0 && sb_n >= 0 && sb_k >= 0, EP_ERR_INVALID_ARG, "negative scale stride");
   EP_REQUIRE(sa_m < kMaxScaleStride, EP_ERR_UNSUPPORTED, "the row stride of a's scales must be below 2^21");
-  EP_REQUIRE(sb_n < ((int64_t)1 << 29), EP_ERR_UNSUPPORTED, "the row stride of b's scales must be below 2^29");
+  // (a tile's second scale ends inside a window of 2^31 - 1 bytes)
+  EP_REQUIRE(sb_n < ((int64_t)1 << 29) - 1, EP_ERR_UNSUPPORTED, "the row stride of b's scales must be below 2^29 - 1");
   EP_REQUIRE(ldd >= n, EP_ERR_INVALID_ARG, "output row stride below the row length");
   const ep_status st = check_elt(out);
   if (st != EP_OK) return st;
