@@ -206,6 +206,8 @@ ep_status ep_expert_dispatch(const void* x, int64_t tokens, int64_t h, int64_t l
                  aligned(scale, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
   EP_REQUIRE(ldx >= h && ldo >= h, EP_ERR_INVALID_ARG, "row stride below the row length");
   EP_REQUIRE(tokens + (rows + 63) / 64 < ((int64_t)1 << 23), EP_ERR_UNSUPPORTED, "too many tokens for one launch");
+  // (copied as 16-bit pieces, 2048 of them to each of at most 65535 workgroups)
+  EP_REQUIRE(scale || elt != EP_ELT_F32 || h <= (int64_t)65535 * 1024, EP_ERR_UNSUPPORTED, "rows of fp32 values have at most 65535 * 1024");
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   ExpertRows p{};
   p.x = x; p.ldx = ldx; p.out = out; p.ldo = ldo; p.pos = pos; p.src = src; p.scale = scale;

@@ -32,3 +32,18 @@ def test_row_stride_of_b_scales():
 def test_row_stride_of_b_scales_below_the_limit(no_gpu):
     assert 4 * (2 ** 29 - 2) + 4 <= 2 ** 31 - 1
     assert matmul(sbn=2 ** 29 - 2) == HIP
+
+
+def dispatch(h, elt, scale=None):
+    return ep.lib().ep_expert_dispatch(P, 4, h, h, elt, P, 2, P, 8, P, h, scale, None)
+
+
+def test_row_length_of_dispatched_fp32():
+    """Rows of fp32 values are copied as twice as many 16-bit pieces, 2048 a workgroup, 65535 workgroups at most."""
+    assert dispatch(65535 * 1024 + 1, 2) == UNSUPPORTED
+    assert all(dispatch(2 ** 26, elt, s) == UNSUPPORTED for elt in (0, 1, 2) for s in (None, P))
+
+
+def test_row_length_of_dispatched_rows_below_the_limits(no_gpu):
+    assert dispatch(65535 * 1024, 2) == HIP
+    assert all(dispatch(2 ** 26 - 1, *a) == HIP for a in ((0,), (1,), (2, P)))
