@@ -51,6 +51,16 @@ ep_status check_product(int64_t rows_a, int64_t rows_b, int64_t k, const void* a
   return EP_OK;
 }
 
+// 128 x 128 tiles of 256 threads, one a workgroup, in a launch of fewer than 2^32 threads.  (The kernels that walk
+// larger tiles have fewer.)
+ep_status check_tiles(int64_t tiles_m, int64_t tiles_n, int64_t parts) {
+  constexpr int64_t kMost = ((int64_t)1 << 24) - 1;
+  EP_REQUIRE(tiles_m * tiles_n <= kMost && tiles_m * tiles_n * parts <= kMost, EP_ERR_UNSUPPORTED,
+             "the output has too many tiles for one launch");
+  return EP_OK;
+}
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
+
 // Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 20 us; 16 rows in
 // tiles with K ranges 26) and up to 4 rows an expert on average (64 experts, n 4096, k 5120: 32 rows in 90 us, 109 in
 // tiles, 256 rows in 220 and 229, 384 rows even).
@@ -104,6 +114,7 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
   p.kb_per_split = (int)((k + 127) / 128);
   const bool rows = m <= kRowsPath;
   if (!rows) {
+    if ((st = check_tiles(tiles_of(m), tiles_of(n), 1)) != EP_OK) return st;
     p.splits = fp8_splits(p.M, p.N, p.K);
     if (p.splits > 1) {
       EP_REQUIRE(workspace && workspace_bytes >= (size_t)p.splits * m * n * 4, EP_ERR_INVALID_ARG,
@@ -129,6 +140,8 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
   EP_REQUIRE(experts < 65535, EP_ERR_UNSUPPORTED, "at most 65534 experts");
   EP_REQUIRE(aligned(offsets, 4), EP_ERR_INVALID_ARG, "misaligned offsets");
   EP_REQUIRE(b_e >= 0 && sb_e >= 0 && b_e % 16 == 0, EP_ERR_INVALID_ARG, "the expert stride of b must be a multiple of 16");
+  const bool few = few_rows(rows, experts);
+  if (!few && (st = check_tiles(tiles_of(rows) + (experts < rows ? experts : rows) + 1, tiles_of(n), 1)) != EP_OK) return st;
   Fp8Gemm p{};
   if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
   p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;
@@ -138,7 +151,7 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
   p.offsets = offsets; p.experts = (int)experts;
   p.M = (int)rows; p.N = (int)n; p.K = (int)k;
   p.splits = 1;
-  if (few_rows(rows, experts))
+  if (few)
     return done(launch_fp8_rows(GM_GROUPED, out, p, (hipStream_t)stream), "grouped_matmul_fp8");
   return done(launch_fp8_tiles(GM_GROUPED, out, p, (hipStream_t)stream), "grouped_matmul_fp8");
 }
@@ -152,6 +165,7 @@ ep_status ep_grouped_wgrad_fp8(int64_t m, int64_t n, int64_t rows, int64_t exper
   EP_REQUIRE(experts >= 1 && offsets, EP_ERR_INVALID_ARG, "at least one expert and its offsets are needed");
   EP_REQUIRE(experts < 65535, EP_ERR_UNSUPPORTED, "at most 65534 experts");
   EP_REQUIRE(aligned(offsets, 4), EP_ERR_INVALID_ARG, "misaligned offsets");
+  if ((st = check_tiles(tiles_of(m), tiles_of(n), experts)) != EP_OK) return st;
   Fp8Gemm p{};
   if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
   p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;

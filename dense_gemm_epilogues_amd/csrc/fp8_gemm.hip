@@ -930,6 +930,7 @@ __global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Fp8Gemm p) {
   }
 }
 
+// (fewer than 2^24, which the C ABI has checked)
 template <int MODE, int BM, int BN>
 int64_t count_tiles(Fp8Gemm& p) {
   p.tiles_n = (p.N + BN - 1) / BN;
@@ -942,7 +943,6 @@ int64_t count_tiles(Fp8Gemm& p) {
 template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int PER_CU>
 hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
   const int64_t tiles = count_tiles<MODE, BM, BN>(p);
-  if (tiles >= 0x7fffffffLL / 512) return hipErrorInvalidConfiguration;
   const int whole = (p.cus >= 8 ? p.cus & ~7 : 8) * PER_CU;
   fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, 2><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
   return hipGetLastError();
@@ -951,7 +951,6 @@ hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
 template <int MODE, int OT>
 hipError_t launch_wide(Fp8Gemm& p, hipStream_t s) {
   const int64_t tiles = count_tiles<MODE, 128, 128>(p);
-  if (tiles >= 0x7fffffffLL / 512) return hipErrorInvalidConfiguration;
   fp8_wide_kernel<MODE, OT, 128, 128, 2, 2><<<(unsigned)tiles, 256, 0, s>>>(p);
   return hipGetLastError();
 }

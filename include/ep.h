@@ -306,7 +306,7 @@ ep_status ep_quantize_fp8(const void* x, int64_t m, int64_t k, int64_t ldx, int 
  * point, 14 bits below the largest of them, before fp32: about 1.5e-5 of the result's norm.)  a: m x k, b: n x k
  * e4m3, 16-byte aligned, row strides multiples of 16 below 2^23, k a multiple of 16; the last block of 128 may be
  * partly filled.  Scale (i, c) is sa[i * sa_m + c * sa_k], scale (j, c) sb[j * sb_n + c * sb_k]; sa_m below 2^21,
- * sb_n below 2^29 - 1.  The workspace (16-byte aligned, of ep_matmul_fp8_workspace bytes, possibly none) holds the
+ * sb_n below 2^29 - 1; the output has fewer than 2^24 tiles of 128 x 128, those of all experts counted.  The workspace (16-byte aligned, of ep_matmul_fp8_workspace bytes, possibly none) holds the
  * sums of K ranges where few tiles leave compute units idle; they are joined in a fixed order. */
 ep_status ep_matmul_fp8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
 ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m,

@@ -4,6 +4,8 @@ import pytest
 import torch
 
 import dense_gemm_epilogues_amd as ep
+from tests import _fp8 as R
+from tests._gpu import require_gpu
 
 INVALID, UNSUPPORTED, HIP = 1, 2, 4
 P = 0x100000
@@ -47,3 +49,46 @@ def test_row_length_of_dispatched_fp32():
 def test_row_length_of_dispatched_rows_below_the_limits(no_gpu):
     assert dispatch(65535 * 1024, 2) == HIP
     assert all(dispatch(2 ** 26 - 1, *a) == HIP for a in ((0,), (1,), (2, P)))
+
+
+def grouped(rows, n, e):
+    return ep.lib().ep_grouped_matmul_fp8(rows, n, 256, e, P, P, 256, P, 1, rows, P, n * 256, 256, P, n, 2, 1, P, n, 1, None)
+
+
+def wgrad(m, n, e):
+    return ep.lib().ep_grouped_wgrad_fp8(m, n, 256, e, P, P, 256, P, 1, m, P, 256, P, 2, 1, P, n, 1, None)
+
+
+TILES = 2 ** 24
+
+
+def test_more_tiles_than_one_launch_takes():
+    """2^24 tiles of 128 x 128 and more are refused; a product of their counts does not overflow."""
+    assert matmul(m=2 ** 18, n=2 ** 20, ldd=2 ** 20) == UNSUPPORTED
+    assert matmul(m=2 ** 30, n=2 ** 30, ldd=2 ** 30) == UNSUPPORTED
+    assert grouped(2 ** 18, 128 * (TILES // (2 ** 11 + 65) + 1), 64) == UNSUPPORTED
+    assert wgrad(128 * 64, 128 * 64, TILES // 4096) == UNSUPPORTED
+    assert wgrad(2 ** 31 - 8192, 2 ** 31 - 8192, 65534) == UNSUPPORTED
+
+
+def test_most_tiles_one_launch_takes(no_gpu):
+    assert matmul(m=2 ** 18, n=2 ** 20 - 128, ldd=2 ** 20) == HIP
+    assert grouped(2 ** 18, 128 * (TILES // (2 ** 11 + 65)), 64) == HIP
+    assert wgrad(128 * 64, 128 * 64, TILES // 4096 - 1) == HIP
+
+
+@pytest.mark.gpu
+def test_product_of_many_tiles():
+    """More than 2^22 tiles, one a workgroup."""
+    require_gpu()
+    g = torch.Generator()
+    g.manual_seed(1)
+    m, n, k = 2 ** 29 + 1000, 8, 16
+    tail, b = R.operand(g, 200, k), R.operand(g, n, k)
+    a = torch.zeros((m, k), dtype=R.F8, device="cuda")
+    a[-200:] = tail.cuda()
+    sa, sb = torch.full((1, 1), 0.5), R.scales(g, 1, 1)
+    d = ep.matmul_fp8(a, sa.cuda().expand(m, 1), b.cuda(), sb.cuda())
+    exact, mags = R.product(tail, sa.expand(200, 1), b, sb)
+    R.assert_within(d[-200:], exact, R.product_tolerance(exact, mags, k, torch.bfloat16))
+    assert not d[:-200].any()
