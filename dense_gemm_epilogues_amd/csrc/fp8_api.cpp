@@ -63,9 +63,12 @@ int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
 // Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 20 us; 16 rows in
 // tiles with K ranges 26) and up to 4 rows an expert on average (64 experts, n 4096, k 5120: 32 rows in 90 us, 109 in
-// tiles, 256 rows in 220 and 229, 384 rows even).
+// tiles, 256 rows in 220 and 229, 384 rows even).  A workgroup of 256 threads takes 16 columns, so from 2^28 columns
+// on, where a launch would pass 2^32 threads, tiles take these too.
 constexpr int64_t kRowsPath = 8;
-bool few_rows(int64_t rows, int64_t experts) { return rows <= 4 * experts; }
+constexpr int64_t kRowsColumns = ((int64_t)1 << 28) - 16;
+bool few_rows(int64_t rows, int64_t n, int64_t experts) { return rows <= 4 * experts && n <= kRowsColumns; }
+bool few_rows(int64_t rows, int64_t n) { return rows <= kRowsPath && n <= kRowsColumns; }
 
 }  // namespace
 
@@ -93,7 +96,7 @@ ep_status ep_matmul_fp8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes
   api_clear();
   EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
   *bytes = 0;
-  if (m < 1 || n < 1 || k < 1 || m >= kMaxCount || n >= kMaxCount || k >= kMaxLd8 || m <= kRowsPath) return EP_OK;
+  if (m < 1 || n < 1 || k < 1 || m >= kMaxCount || n >= kMaxCount || k >= kMaxLd8 || few_rows(m, n)) return EP_OK;
   const int s = fp8_splits((int)m, (int)n, (int)k);
   if (s > 1) *bytes = (size_t)s * m * n * 4;
   return EP_OK;
@@ -112,7 +115,7 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
   p.M = (int)m; p.N = (int)n; p.K = (int)k;
   p.splits = 1;
   p.kb_per_split = (int)((k + 127) / 128);
-  const bool rows = m <= kRowsPath;
+  const bool rows = few_rows(m, n);
   if (!rows) {
     if ((st = check_tiles(tiles_of(m), tiles_of(n), 1)) != EP_OK) return st;
     p.splits = fp8_splits(p.M, p.N, p.K);
@@ -140,7 +143,7 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
   EP_REQUIRE(experts < 65535, EP_ERR_UNSUPPORTED, "at most 65534 experts");
   EP_REQUIRE(aligned(offsets, 4), EP_ERR_INVALID_ARG, "misaligned offsets");
   EP_REQUIRE(b_e >= 0 && sb_e >= 0 && b_e % 16 == 0, EP_ERR_INVALID_ARG, "the expert stride of b must be a multiple of 16");
-  const bool few = few_rows(rows, experts);
+  const bool few = few_rows(rows, n, experts);
   if (!few && (st = check_tiles(tiles_of(rows) + (experts < rows ? experts : rows) + 1, tiles_of(n), 1)) != EP_OK) return st;
   Fp8Gemm p{};
   if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;

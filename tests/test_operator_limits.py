@@ -92,3 +92,26 @@ def test_product_of_many_tiles():
     exact, mags = R.product(tail, sa.expand(200, 1), b, sb)
     R.assert_within(d[-200:], exact, R.product_tolerance(exact, mags, k, torch.bfloat16))
     assert not d[:-200].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["matmul", "grouped"])
+@pytest.mark.parametrize("n", [2 ** 28 - 16, 2 ** 28 + 5])
+def test_few_rows_by_many_columns(call, n):
+    """The longest output rows of the kernel that streams b past a few rows, and longer ones."""
+    require_gpu()
+    g = torch.Generator()
+    g.manual_seed(2)
+    m, k = 3, 16
+    a, tail = R.operand(g, m, k), R.operand(g, 200, k)
+    b = torch.zeros((n, k), dtype=R.F8, device="cuda")
+    b[-200:] = tail.cuda()
+    sa, sb = R.scales(g, m, 1), torch.full((1, 1), 0.5)
+    ops = (a.cuda(), sa.cuda(), b, sb.cuda().expand(R.blocks(n), 1))
+    if call == "matmul":
+        d = ep.matmul_fp8(*ops)
+    else:
+        d = ep.grouped_matmul_fp8(*ops[:2], b[None], ops[3][None], torch.tensor([0, m], dtype=torch.int32, device="cuda"))
+    exact, mags = R.product(a, sa, tail, sb.expand(2, 1))
+    R.assert_within(d[:, -200:], exact, R.product_tolerance(exact, mags, k, torch.bfloat16))
+    assert not d[:, :-200].any()
