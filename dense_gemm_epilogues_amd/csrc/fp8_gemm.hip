@@ -258,7 +258,7 @@ struct Tiles {
       t.kb0 = r0 / kScaleBlock;
       t.nkb = r1 / kScaleBlock - t.kb0;
       t.klen = r1;
-      if ((r0 | r1) % kScaleBlock) {  // such a group has no scales of its own
+      if (r0 < r1 && (r0 | r1) % kScaleBlock) {  // such a group has no scales of its own
         t.nkb = 0;
         t.fill = __builtin_nanf("");
       }

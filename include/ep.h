@@ -326,7 +326,7 @@ ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t expe
  * columns, with scales per row of a and 128 rows of b by 128 columns; D[e] (m x n, row stride ldd, one
  * expert m * ldd behind another) = sum over columns r = offsets[e] .. offsets[e + 1] - 1 of
  * a[.][r] b[.][r] with their scales.  Groups start and end on multiples of 128 (the gradient of one that
- * does not is NaN); an empty group's gradient is zero. */
+ * does not is NaN); an empty group's gradient is zero, wherever it lies. */
 ep_status ep_grouped_wgrad_fp8(int64_t m, int64_t n, int64_t rows, int64_t experts, const int32_t* offsets, const void* a,
                                int64_t lda, const float* sa, int64_t sa_m, int64_t sa_k, const void* b, int64_t ldb,
                                const float* sb, int64_t sb_n, int64_t sb_k, void* d, int64_t ldd, int out, void* stream);

@@ -55,3 +55,20 @@ def test_each_row_has_one_group_at_most(kernel, kind, dtype):
             want = (x[at] @ R.dequantized(b[i], sb[i], 128).t()).to(dtype)
             assert torch.equal(buf[pad:pad + rows][at], want), f"expert {i}, rows {at.start} to {at.stop}"
     assert not buf[pad + ends[-1]:pad + rows].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n", [(48, 80), (1100, 4100)])
+def test_empty_group_off_the_blocks_has_a_zero_gradient(m, n, dtype):
+    """Next to groups whose gradient is NaN because they start or end off the scale blocks."""
+    require_gpu()
+    g = torch.Generator()
+    g.manual_seed(m)
+    rows, off = 512, [0, 0, 128, 200, 200, 200, 256, 512, 512, 300]
+    operand = lambda *s: R.operand(g, *s).cuda()  # noqa: E731
+    d = ep.grouped_wgrad_fp8(operand(m, rows), R.scales(g, m, 4).cuda(), operand(n, rows), R.scales(g, R.blocks(n), 4).cuda(),
+                             torch.tensor(off, dtype=torch.int32, device="cuda"), out_dtype=dtype)
+    for i in (0, 3, 4, 7, 8):
+        assert not d[i].any(), f"group {i}"
+    assert d[2].isnan().all() and d[5].isnan().all()
+    assert d[1].isfinite().all() and d[1].any() and d[6].isfinite().all() and d[6].any()
