@@ -85,8 +85,8 @@ ep_status ep_quantize_fp8(const void* x, int64_t m, int64_t k, int64_t ldx, int 
   EP_REQUIRE(block_rows == 1 || block_rows == 128, EP_ERR_UNSUPPORTED, "scale blocks are 1 x 128 or 128 x 128");
   EP_REQUIRE(aligned(x, elt_size(elt)) && aligned(scale, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
   EP_REQUIRE(ldx >= k && ldq >= (transpose ? m : k), EP_ERR_INVALID_ARG, "row stride below the row length");
-  const int64_t tiles = ((k + 127) / 128) * ((m + 7) / 8);
-  EP_REQUIRE(tiles < ((int64_t)1 << 23), EP_ERR_UNSUPPORTED, "the matrix has too many blocks for one launch");
+  EP_REQUIRE(quantize_blocks(block_rows, transpose != 0, m, k) < ((int64_t)1 << 24), EP_ERR_UNSUPPORTED,
+             "the matrix has too many blocks for one launch");  // (workgroups of 256 threads, fewer than 2^32 of those)
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   QuantArgs p{x, ldx, (int)m, (int)k, (uint8_t*)q, ldq, scale};
   return done(launch_quantize(elt, block_rows, transpose != 0, p, (hipStream_t)stream), "quantize_fp8");

@@ -48,6 +48,11 @@ struct QuantArgs {
   int64_t ldq;
   float* scale;                      // rows 1: [ceil][rows], features outermost; rows 128: [blocks][blocks]
 };
+// workgroups of a quantisation (m x k as given): 8 rows by 4 blocks of 1 x 128 each, or a tile of 128 x 128
+constexpr int64_t quantize_blocks(int rows, bool transpose, int64_t m, int64_t k) {
+  const int64_t kb = (k + kScaleBlock - 1) / kScaleBlock;
+  return rows == 1 && !transpose ? (kb + 3) / 4 * ((m + 7) / 8) : kb * ((m + kScaleBlock - 1) / kScaleBlock);
+}
 hipError_t launch_quantize(int elt, int rows, bool transpose, const QuantArgs& p, hipStream_t s);
 
 struct OrderArgs {

@@ -179,17 +179,12 @@ __global__ __launch_bounds__(kThreads) void quantize_tile_kernel(QuantArgs p, in
 
 template <int E>
 hipError_t launch_e(int rows, bool transpose, const QuantArgs& p, hipStream_t s) {
-  const int tk = (p.k + kScaleBlock - 1) / kScaleBlock, tm = (p.m + kScaleBlock - 1) / kScaleBlock;
-  if (rows == 1 && !transpose) {
-    const int kbg = (tk + 3) / 4;
-    const unsigned blocks = (unsigned)((int64_t)kbg * ((p.m + 7) / 8));
-    quantize_rows_kernel<E><<<blocks, kThreads, 0, s>>>(p, kbg);
-  } else {
-    const unsigned blocks = (unsigned)((int64_t)tk * tm);
-    if (rows == 1) quantize_tile_kernel<E, 1, true><<<blocks, kThreads, 0, s>>>(p, tk);
-    else if (transpose) quantize_tile_kernel<E, 128, true><<<blocks, kThreads, 0, s>>>(p, tk);
-    else quantize_tile_kernel<E, 128, false><<<blocks, kThreads, 0, s>>>(p, tk);
-  }
+  const int tk = (p.k + kScaleBlock - 1) / kScaleBlock;
+  const unsigned blocks = (unsigned)quantize_blocks(rows, transpose, p.m, p.k);
+  if (rows == 1 && !transpose) quantize_rows_kernel<E><<<blocks, kThreads, 0, s>>>(p, (tk + 3) / 4);
+  else if (rows == 1) quantize_tile_kernel<E, 1, true><<<blocks, kThreads, 0, s>>>(p, tk);
+  else if (transpose) quantize_tile_kernel<E, 128, true><<<blocks, kThreads, 0, s>>>(p, tk);
+  else quantize_tile_kernel<E, 128, false><<<blocks, kThreads, 0, s>>>(p, tk);
   return hipGetLastError();
 }
 

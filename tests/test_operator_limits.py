@@ -115,3 +115,48 @@ def test_few_rows_by_many_columns(call, n):
     exact, mags = R.product(a, sa, tail, sb.expand(2, 1))
     R.assert_within(d[:, -200:], exact, R.product_tolerance(exact, mags, k, torch.bfloat16))
     assert not d[:, :-200].any()
+
+
+def quantize(m, k, rows, transpose):
+    return ep.lib().ep_quantize_fp8(P, m, k, k, 1, rows, transpose, P, m if transpose else k, P, None)
+
+
+# (rows of a block, transposed), and what a workgroup takes: 8 rows by 4 blocks, or 128 x 128 values
+WORKGROUPS = [(1, 0, 8, 512), (1, 1, 128, 128), (128, 0, 128, 128), (128, 1, 128, 128)]
+
+
+@pytest.mark.parametrize("rows,transpose,by_m,by_k", WORKGROUPS)
+def test_more_blocks_than_one_launch_quantises(rows, transpose, by_m, by_k):
+    assert quantize(by_m * 4096, by_k * 4096, rows, transpose) == UNSUPPORTED
+    assert quantize(by_m * 5000, by_k * 4000, rows, transpose) == UNSUPPORTED
+    assert quantize(2 ** 31 - 8192, 2 ** 31 - 8192, rows, transpose) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows,transpose,by_m,by_k", WORKGROUPS)
+def test_most_blocks_one_launch_quantises(no_gpu, rows, transpose, by_m, by_k):
+    """All the workgroups that a launch takes, whatever the kind of block."""
+    assert quantize(by_m * 4096, by_k * 4095, rows, transpose) == HIP
+    assert quantize(by_m * 4095, by_k * 4096, rows, transpose) == HIP
+    assert quantize(2 ** 26 + 9, 16, rows, transpose) == HIP  # (narrow, with 2^23 times 8 rows)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,transpose,by_m,by_k", WORKGROUPS)
+def test_quantise_of_many_rows(rows, transpose, by_m, by_k):
+    """2^26 narrow rows: the last ones are right, and where the rows before them are zeros, so are their values."""
+    require_gpu()
+    g = torch.Generator()
+    g.manual_seed(3)
+    m, k = 2 ** 26 + 9, 16
+    last = 128 + m % 128
+    x = torch.zeros((m, k), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn((last, k), generator=g).bfloat16()
+    x[-last:] = tail.cuda()
+    q, s = ep.quantize_fp8(x, block=(rows, 128), transpose=bool(transpose))
+    wq, ws = R.quantize(tail, rows, bool(transpose))
+    cut = (slice(None), slice(-last, None)) if transpose else (slice(-last, None),)
+    assert torch.equal(q[cut].float().cpu(), wq)
+    n = ws.shape[1] if transpose else ws.shape[0]
+    assert torch.equal((s[:, -n:] if transpose else s[-n:]).cpu(), ws)
+    rest = (slice(None), slice(None, -last)) if transpose else (slice(None, -last),)
+    assert not q[rest].contiguous().view(torch.uint8).any()
