@@ -1,6 +1,7 @@
 """What the 8-bit and expert operators share: the C ABI's signatures, argument checks, streams."""
 import ctypes
 import inspect
+import warnings
 from functools import wraps
 
 import torch
@@ -49,6 +50,14 @@ def check(name, t, dtypes, shape, device=None):
         raise ValueError(f"{name} must have shape {want}, got {tuple(s)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other operands are on {device}")
+
+
+def no_gradient(f, *tensors):
+    """Warn where autograd would be expected to follow an argument of f, whose results it does not follow."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            warnings.warn(f"{f} is outside autograd: its result carries no gradient to an argument that requires one", stacklevel=4)
+            return
 
 
 def unit_columns(name, t):

@@ -8,7 +8,8 @@
     dx = expert_combine(drows, order)                     # the gradient of expert_dispatch
 
 Every function only enqueues kernels (libep.so, `ep_expert_*` in include/ep.h) on torch's current stream,
-or on `stream`.
+or on `stream`, as under torch.cuda.stream(stream).  All are outside autograd: results carry no gradient, the gradients
+are the functions above, and a call that autograd would be expected to follow warns.
 """
 import ctypes
 from functools import lru_cache
@@ -17,8 +18,8 @@ from typing import NamedTuple
 import torch
 
 from . import _check, lib
-from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, on_device, streamed,
-                         unit_columns)
+from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
+                         streamed, unit_columns)
 
 __all__ = ["ExpertOrder", "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
 
@@ -87,6 +88,7 @@ def expert_dispatch(x, order, quantize=False, out=None):
     check("x", x, ELT, (None, None))
     t, h = x.shape
     k, rows = _order(order, t, x.device)
+    no_gradient("expert_dispatch", x)
     ldx = unit_columns("x", x)
     on_device(x)
     dtype = E4M3 if quantize else x.dtype
@@ -115,6 +117,7 @@ def expert_combine(y, order, weights=None, out=None):
         raise ValueError(f"y must have the order's {cap} rows, got {rows}")
     ldy = unit_columns("y", y)
     w, ldw = _weights(weights, t, k, y.device)
+    no_gradient("expert_combine", y, weights)
     on_device(y)
     if out is None:
         out, ldo = torch.empty((t, h), dtype=y.dtype, device=y.device), h
@@ -138,6 +141,7 @@ def expert_combine_backward(dout, y, order, weights=None):
         raise ValueError(f"y must have the order's {rows} rows, got {y.shape[0]}")
     ldy, ldo = unit_columns("y", y), unit_columns("dout", dout)
     w, ldw = _weights(weights, t, k, y.device)
+    no_gradient("expert_combine_backward", dout, y, weights)
     on_device(y)
     dy = torch.empty((rows, h), dtype=y.dtype, device=y.device)
     dw = torch.empty((t, k), dtype=torch.float32, device=y.device)

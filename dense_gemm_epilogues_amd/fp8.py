@@ -8,7 +8,9 @@ A matrix in this form is a pair (q, scale): q e4m3 values, scale one fp32 number
     y = matmul_fp8(xq, xs, wq, ws)                        # x w^T
 
 Every function only enqueues kernels (libep.so, `ep_*_fp8` in include/ep.h) on torch's current stream, or
-on `stream`.
+on `stream`, as under torch.cuda.stream(stream).  All are outside autograd: results carry no gradient, and a call
+that autograd would be expected to follow warns.  The gradients of y = x w^T are products of the transposes:
+dy w by matmul_fp8 and grouped_matmul_fp8, dy^T x by grouped_wgrad_fp8 (one expert: matmul_fp8).
 """
 import ctypes
 from functools import lru_cache
@@ -16,8 +18,8 @@ from functools import lru_cache
 import torch
 
 from . import _check, lib
-from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, on_device, streamed,
-                         unit_columns)
+from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
+                         streamed, unit_columns)
 
 __all__ = ["quantize_fp8", "matmul_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8"]
 
@@ -32,6 +34,7 @@ def quantize_fp8(x, block=(1, BLOCK), transpose=False):
     check("x", x, ELT, (None, None))
     if tuple(block) not in ((1, BLOCK), (BLOCK, BLOCK)):
         raise ValueError(f"block must be (1, 128) or (128, 128), got {block}")
+    no_gradient("quantize_fp8", x)
     ld = unit_columns("x", x)
     on_device(x)
     m, k = x.shape
@@ -90,6 +93,7 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
     lda, ldb = _operand("a", a, (m, k)), _operand("b", b, (n, k))
     check("a_scale", a_scale, torch.float32, (m, blocks(k)), a.device)
     check("b_scale", b_scale, torch.float32, (blocks(n), blocks(k)), a.device)
+    no_gradient("matmul_fp8", a, a_scale, b, b_scale)
     on_device(a)
     out, ldd = _out(out, out_dtype, (m, n), a, (a, a_scale, b, b_scale))
     if not m or not n:
@@ -128,6 +132,7 @@ def grouped_matmul_fp8(a, a_scale, b, b_scale, offsets, out_dtype=torch.bfloat16
     check("a_scale", a_scale, torch.float32, (rows, blocks(k)), a.device)
     check("b_scale", b_scale, torch.float32, (e, blocks(n), blocks(k)), a.device)
     _offsets(offsets, e, a.device)
+    no_gradient("grouped_matmul_fp8", a, a_scale, b, b_scale)
     on_device(a)
     out, ldd = _out(out, out_dtype, (rows, n), a, (a, a_scale, b, b_scale, offsets))
     if not rows or not n:
@@ -156,6 +161,7 @@ def grouped_wgrad_fp8(a, a_scale, b, b_scale, offsets, out_dtype=torch.bfloat16,
     check("a_scale", a_scale, torch.float32, (m, blocks(rows)), a.device)
     check("b_scale", b_scale, torch.float32, (blocks(n), blocks(rows)), a.device)
     e = _offsets(offsets, None, a.device)
+    no_gradient("grouped_wgrad_fp8", a, a_scale, b, b_scale)
     on_device(a)
     out, ldd = _out(out, out_dtype, (e, m, n), a, (a, a_scale, b, b_scale, offsets))
     if e > 1 and m and out.stride(0) != m * ldd:

@@ -1,5 +1,6 @@
 """How the 8-bit and expert operators can be called (CPU): every argument by its name, `stream` among them."""
 import inspect
+import warnings
 from types import SimpleNamespace
 
 import pytest
@@ -59,3 +60,22 @@ def test_stream_of_another_device_is_refused(f):
         on_gpu = torch.empty(first[1].shape, dtype=first[1].dtype, device="cuda:0")
         with pytest.raises(ValueError, match="the stream is on cuda:1"):
             f(**{first[0]: on_gpu}, **dict(rest), stream=SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+@pytest.mark.parametrize("f", [f for f in calls() if f is not ep.expert_order], ids=lambda f: f.__name__)
+def test_a_lost_gradient_warns(f):
+    """The operators are outside autograd: where it would be expected to follow an argument, they say so."""
+    kw = calls()[f]
+    for name, t in kw.items():
+        if not (isinstance(t, torch.Tensor) and t.is_floating_point()):
+            continue
+        some = {**kw, name: t.clone().requires_grad_()}
+        with pytest.warns(UserWarning, match=f"{f.__name__} is outside autograd") as seen, pytest.raises(ValueError, match="CUDA"):
+            f(**some)
+        assert seen[0].filename == __file__  # (points at the call)
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            with pytest.raises(ValueError, match="CUDA"), torch.no_grad():
+                f(**some)
+            with pytest.raises(ValueError, match="CUDA"):
+                f(**kw)
