@@ -63,7 +63,8 @@ int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
 // Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 20 us; 16 rows in
 // tiles with K ranges 26) and up to 4 rows an expert on average (64 experts, n 4096, k 5120: 32 rows in 90 us, 109 in
-// tiles, 256 rows in 220 and 229, 384 rows even).  A workgroup of 256 threads takes 16 columns, so from 2^28 columns
+// tiles, 256 rows in 220 and 229, 384 rows even).  The offsets are on the device, so the largest group is not known
+// here: 256 rows, all of one expert, take 139 us (28 in tiles), half of them 249 (232).  A workgroup of 256 threads takes 16 columns, so from 2^28 columns
 // on, where a launch would pass 2^32 threads, tiles take these too.
 constexpr int64_t kRowsPath = 8;
 constexpr int64_t kRowsColumns = ((int64_t)1 << 28) - 16;

@@ -72,3 +72,20 @@ def test_empty_group_off_the_blocks_has_a_zero_gradient(m, n, dtype):
         assert not d[i].any(), f"group {i}"
     assert d[2].isnan().all() and d[5].isnan().all()
     assert d[1].isfinite().all() and d[1].any() and d[6].isfinite().all() and d[6].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("experts", [64, 300])
+def test_few_rows_all_on_one_expert(experts, dtype):
+    """As many rows as the few-row kernel takes (4 an expert), on the first, one in the middle or the last expert."""
+    require_gpu()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(experts)
+    rows, n, k = 4 * experts, 130, 656
+    whole = lambda *s: torch.randint(-2, 3, s, generator=g, device="cuda").float().to(R.F8)  # noqa: E731
+    a, b = whole(rows, k), whole(experts, n, k)
+    sa, sb = torch.full((rows, 6), 0.5, device="cuda"), torch.full((experts, 2, 6), 2.0, device="cuda")
+    for one in (0, experts // 2, experts - 1):
+        off = torch.tensor([0] * (one + 1) + [rows] * (experts - one), dtype=torch.int32, device="cuda")
+        d = ep.grouped_matmul_fp8(a, sa, b, sb, off, out_dtype=dtype)
+        assert torch.equal(d, (R.dequantized(a, sa) @ R.dequantized(b[one], sb[one], 128).t()).to(dtype)), f"expert {one}"
