@@ -998,7 +998,7 @@ hipError_t launch_rows(Fp8Gemm& p, hipStream_t s) {
 
 // K ranges of a product with few tiles.  A step of 128 x 128 tiles takes 0.6 us with two of them on every compute
 // unit; ranges cost a launch (5 us) and their parts' way through memory, written and read at about 4 TB/s.  By
-// this model 64 x 5120 x 5120 takes 5 ranges (19 us, unsplit 27), 128 x 5120 x 17408 takes 10 (84 us unsplit),
+// this model 64 x 5120 x 5120 takes 5 ranges (19 us, unsplit 27), 128 x 5120 x 17408 takes 8 (31 us, unsplit 84),
 // 1024 x 4096 x 5120 none (30 us, 37 with 2).
 int fp8_splits(int m, int n, int k) {
   const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 127) / 128);

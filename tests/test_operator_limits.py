@@ -1,5 +1,7 @@
 """Largest sizes and strides of the 8-bit and expert operators.  On the CPU: the C ABI's refusals, which come
 before any HIP call (pointers are fake and never read)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -160,3 +162,11 @@ def test_quantise_of_many_rows(rows, transpose, by_m, by_k):
     assert torch.equal((s[:, -n:] if transpose else s[-n:]).cpu(), ws)
     rest = (slice(None), slice(None, -last)) if transpose else (slice(None, -last),)
     assert not q[rest].contiguous().view(torch.uint8).any()
+
+
+@pytest.mark.parametrize("m,n,k,parts", [(128, 5120, 17408, 8), (64, 5120, 5120, 5), (1024, 4096, 5120, 0), (777, 5003, 4112, 0), (8, 5120, 17408, 0)])
+def test_k_ranges(m, n, k, parts):
+    """How many K ranges a product takes, by its workspace; none where that is no gain, or b streams past few rows."""
+    need = ctypes.c_size_t()
+    assert ep.lib().ep_matmul_fp8_workspace(m, n, k, ctypes.byref(need)) == 0
+    assert need.value == parts * m * n * 4
