@@ -3,7 +3,7 @@
 //
 // Every kernel but the order is bound by HBM: it is one pass over the expert rows, walked by token, so
 // that a token's row is read (or written) once whatever the number of its choices.  8192 tokens, 8 of 64 experts,
-// 5120 bf16 features: combined in 130 us (5.6 TB/s), their gradients in 298 (4.7), ordered and dispatched in 159
+// 5120 bf16 features: combined in 132 us (5.5 TB/s), their gradients in 297 (4.7), ordered and dispatched in 159
 // (the order 14 of them); a large device copy reaches 5.1 TB/s, a fill 6.9.
 #include "fp8_device.hpp"
 
@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kOrderThreads) void order_count_kernel(OrderArgs p)
 
 template <bool ONE>
 __global__ __launch_bounds__(kOrderThreads) void order_place_kernel(OrderArgs p) {
-  __shared__ int total[kMaxExperts];           // slots of each expert, then its first row
+  __shared__ int total[kMaxExperts];           // slots of each expert
   __shared__ int next[kMaxExperts];            // rows this workgroup's next slots of each expert take
   __shared__ int cnt[kOrderWaves][kMaxExperts];
   __shared__ int part[kOrderWaves];
@@ -167,7 +167,8 @@ constexpr int kSpan = kThreads * 8;
 constexpr int kPadRows = 64;
 
 // Expert rows that no cache holds (the Infinity Cache is 256 MB) pass non-temporally: 8192 tokens to 64 experts,
-// 8 choices, 5120 features, dispatched in 162 us (181 without), combined in 133 (151), the gradients in 311 (320).
+// 8 choices, 5120 features, ordered and dispatched in 159 us (180 without), combined in 132 (150), the gradients in
+// 297 (317).
 // Smaller ones are likely in a cache when the next kernel reads them.
 constexpr int64_t kStreamBytes = (int64_t)256 << 20;
 bool streams(int elt, const ExpertRows& p) { return (int64_t)p.rows * p.h * elt_size(elt) > kStreamBytes; }

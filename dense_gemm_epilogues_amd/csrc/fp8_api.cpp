@@ -61,10 +61,11 @@ ep_status check_tiles(int64_t tiles_m, int64_t tiles_n, int64_t parts) {
 }
 int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
-// Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 20 us; 16 rows in
-// tiles with K ranges 26) and up to 4 rows an expert on average (64 experts, n 4096, k 5120: 32 rows in 90 us, 109 in
-// tiles, 256 rows in 220 and 229, 384 rows even).  The offsets are on the device, so the largest group is not known
-// here: 256 rows, all of one expert, take 139 us (28 in tiles), half of them 249 (232).  A workgroup of 256 threads takes 16 columns, so from 2^28 columns
+// Products that stream b past a few rows, without tiles: matmuls of up to 8 rows (8 x 17408 x 5120 in 19.5 us, 25 in
+// tiles with K ranges; 16 rows 32, 25.5 in tiles; operands that no cache holds) and up to 4 rows an expert on average (64
+// experts, n 4096, k 5120: 8 rows in 27 us, 33 in tiles, 32 rows in 107 and 117, 256 in 216 and 228, 384 even).  The
+// offsets are on the device, so the largest group is not known here: 256 rows, all of one expert, take 137 us (28.5 in
+// tiles), half of them as long as in tiles (251).  A workgroup of 256 threads takes 16 columns, so from 2^28 columns
 // on, where a launch would pass 2^32 threads, tiles take these too.
 constexpr int64_t kRowsPath = 8;
 constexpr int64_t kRowsColumns = ((int64_t)1 << 28) - 16;

@@ -411,8 +411,8 @@ __device__ constexpr bool read_first(int j) {
 // waits little between steps.  The steps run on from tile to tile: the next tile's operands land while this
 // one's last steps are multiplied.
 //
-// Measured on one MI355X: 8192 x 17408 x 5120 in 611 us, 2389 TFLOP/s (one tile a workgroup, all loads at a step's
-// start: 667).  What bounds it is power: the card runs it at 1.7 GHz of 2.4, the matrix unit is busy for 60 % of
+// Measured on one MI355X: 8192 x 17408 x 5120 in 602 us, 2426 TFLOP/s (596 to 705 from run to run, by the clock;
+// one tile a workgroup, all loads at a step's start: 667).  What bounds it is power: the card runs it at 1.7 GHz of 2.4, the matrix unit is busy for 60 % of
 // the cycles.  From registers alone the same MFMAs with random operands reach 3863 TFLOP/s, 3484 with their
 // multiply-adds; without the loads (operands left in LDS) a step takes 12 % fewer cycles, without the multiply-adds 15 %.
 template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
@@ -826,8 +826,9 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm p) {
 // Few rows: bound by reading b once.  A workgroup takes 16 rows of b
 // (columns of D) by 8 of a; its waves deal out the scale blocks and join their sums in LDS.  Each wave has a ring
 // of its own in LDS, filled by loads that write it themselves and ordered by the wave's load count alone: what
-// is in flight (6 KB of b a wave, 16 waves a compute unit) takes no registers.  Read at 5.2 TB/s (one token's 8
-// experts, n 4096, k 5120: 32 us; 40 through registers) to 6.4 (4 tokens'); 8 waves a workgroup: 35 us.
+// is in flight (6 KB of b a wave, 16 waves a compute unit) takes no registers.  One token's 8
+// experts, n 4096, k 5120, in 30 us (5.5 TB/s, the inputs changing from pass to pass); the first form through LDS took
+// 32, through registers 40, with 8 waves a workgroup 35.
 constexpr int kRowsWaves = 4;
 template <int MODE, int OT>
 __global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Fp8Gemm p) {
@@ -974,11 +975,11 @@ hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
   }
   if constexpr (OT != EL_F32) {
     if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
-      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 35 us,
-      // 62 with 80 large tiles); with more the large ones, which read half as much through the caches
-      // (8192 x 17408 x 5120: 711 us, 849 with small ones)
+      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 36 us
+      // with operands that no cache holds, 59 with 80 large tiles); with more the large ones, which read half as much
+      // through the caches (8192 x 17408 x 5120: 602 us, 744 with small ones)
       const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
-      // so with few rows an expert: 64 experts of 64 rows, n 4096, k 5120: 255 us, 273 with large tiles (of 128: 355, 287)
+      // so with few rows an expert: 64 experts of 64 rows, n 4096, k 5120: 244 us, 267 with large tiles (of 128: 282, 281)
       if (big < p.cus || (MODE == GM_GROUPED && p.M <= 96 * (int64_t)p.experts)) return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(p, s);
       return launch_tile<MODE, OT, 256, 256, 4, 2, 1>(p, s);
     }
@@ -998,8 +999,8 @@ hipError_t launch_rows(Fp8Gemm& p, hipStream_t s) {
 
 // K ranges of a product with few tiles.  A step of 128 x 128 tiles takes 0.6 us with two of them on every compute
 // unit; ranges cost a launch (5 us) and their parts' way through memory, written and read at about 4 TB/s.  By
-// this model 64 x 5120 x 5120 takes 5 ranges (19 us, unsplit 27), 128 x 5120 x 17408 takes 8 (31 us, unsplit 84),
-// 1024 x 4096 x 5120 none (30 us, 37 with 2).
+// this model 64 x 5120 x 5120 takes 5 ranges (17 us, unsplit 35), 128 x 5120 x 17408 takes 8 (39 us, unsplit 110),
+// 1024 x 4096 x 5120 none (36 us, 40 with 2); operands that no cache holds.
 int fp8_splits(int m, int n, int k) {
   const int64_t tiles = (int64_t)((m + 127) / 128) * ((n + 127) / 128);
   const int blocks = (k + kScaleBlock - 1) / kScaleBlock;
