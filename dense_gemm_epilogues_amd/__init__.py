@@ -12,9 +12,10 @@ plan / execute / free sequence of the pages (nvmath-python's Matmul as described
     dx, aux = dp.execute()        # aux["drelu_bgrad"]: float32 bias gradient
     p.free(); dp.free()
 
-The 8-bit block-scaled products and the expert (mixture-of-experts) operators are plain functions: see
-fp8.py (quantize_fp8, matmul_fp8, grouped_matmul_fp8, grouped_wgrad_fp8) and experts.py (expert_order,
-expert_dispatch, expert_combine, expert_combine_backward).
+The 8-bit block-scaled products, the expert (mixture-of-experts) operators and the norm are plain functions: see
+fp8.py (quantize_fp8, matmul_fp8, epilogue_backward_fp8, grouped_matmul_fp8, grouped_wgrad_fp8), experts.py (expert_route,
+expert_route_backward, expert_order, expert_dispatch, expert_combine, expert_combine_backward) and norm.py (rms_norm,
+rms_norm_backward).
 
 The library is loaded from this package directory; if it has not been built the import
 of the library fails loudly (there is no fallback).
@@ -27,8 +28,9 @@ import torch
 from ._operators import SIGNATURES
 
 __all__ = ["Plan", "EPError", "EPILOGS", "lib", "library_path", "abi_version", "num_tile_cfgs", "validate_operands",
-           "describe_plan", "quantize_fp8", "matmul_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8", "ExpertOrder",
-           "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
+           "describe_plan", "quantize_fp8", "matmul_fp8", "EpilogueGradients", "epilogue_backward_fp8", "grouped_matmul_fp8",
+           "grouped_wgrad_fp8", "ExpertOrder", "expert_route", "expert_route_backward", "expert_order", "expert_dispatch",
+           "expert_combine", "expert_combine_backward", "Normed", "rms_norm", "rms_norm_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # EP_LIBRARY names another build of the same library (the host-sanitizer build the CPU tests use)
@@ -390,6 +392,9 @@ class Plan:
             pass
 
 
-# 8-bit block-scaled products and expert operators (they use the binding above)
-from .experts import ExpertOrder, expert_combine, expert_combine_backward, expert_dispatch, expert_order  # noqa: E402
-from .fp8 import grouped_matmul_fp8, grouped_wgrad_fp8, matmul_fp8, quantize_fp8  # noqa: E402
+# 8-bit block-scaled products, expert operators and the norm (they use the binding above)
+from .experts import (ExpertOrder, expert_combine, expert_combine_backward, expert_dispatch, expert_order, expert_route,  # noqa: E402
+                      expert_route_backward)
+from .fp8 import (EpilogueGradients, epilogue_backward_fp8, grouped_matmul_fp8, grouped_wgrad_fp8, matmul_fp8,  # noqa: E402
+                  quantize_fp8)
+from .norm import Normed, rms_norm, rms_norm_backward  # noqa: E402

@@ -1,4 +1,4 @@
-"""What the 8-bit and expert operators share: the C ABI's signatures, argument checks, streams."""
+"""What the 8-bit, expert and norm operators share: the C ABI's signatures, argument checks, streams."""
 import ctypes
 import inspect
 import warnings
@@ -6,12 +6,15 @@ from functools import wraps
 
 import torch
 
-P, I64, INT, SIZE = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+P, I64, INT, SIZE, F64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
 
 SIGNATURES = {
     "ep_quantize_fp8": [P, I64, I64, I64, INT, INT, INT, P, I64, P, P],
     "ep_matmul_fp8_workspace": [I64, I64, I64, P],
     "ep_matmul_fp8": [I64, I64, I64, P, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, INT, P, SIZE, P],
+    "ep_matmul_fp8_epilog": [I64, I64, I64, P, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, INT, P, INT, INT, P, I64, P, I64, P, SIZE, P],
+    "ep_epilogue_backward_fp8_workspace": [I64, I64, P],
+    "ep_epilogue_backward_fp8": [P, I64, I64, I64, INT, INT, P, I64, P, I64, P, P, I64, P, P, P, SIZE, P],
     "ep_grouped_matmul_fp8": [I64, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, I64, P, I64, I64, I64, P, I64, INT, P],
     "ep_grouped_wgrad_fp8": [I64, I64, I64, I64, P, P, I64, P, I64, I64, P, I64, P, I64, I64, P, I64, INT, P],
     "ep_expert_order_sizes": [I64, I64, I64, P, P],
@@ -19,6 +22,11 @@ SIGNATURES = {
     "ep_expert_dispatch": [P, I64, I64, I64, INT, P, I64, P, I64, P, I64, P, P],
     "ep_expert_combine": [P, I64, I64, I64, INT, P, I64, I64, P, I64, P, I64, P],
     "ep_expert_combine_backward": [P, I64, I64, I64, INT, P, I64, I64, P, I64, P, P, I64, P, I64, P, P],
+    "ep_expert_route": [P, I64, I64, I64, INT, P, INT, I64, I64, INT, I64, INT, F64, P, P, P],
+    "ep_expert_route_backward": [P, I64, I64, I64, P, I64, I64, INT, P, INT, INT, F64, P, I64, P],
+    "ep_rms_norm": [P, I64, I64, I64, INT, P, I64, P, INT, F64, P, I64, P, I64, P, P, P],
+    "ep_rms_norm_backward_workspace": [I64, I64, P],
+    "ep_rms_norm_backward": [P, I64, I64, I64, INT, P, I64, P, INT, P, P, I64, P, I64, P, P, SIZE, P],
 }
 
 ELT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}

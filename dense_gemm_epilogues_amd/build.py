@@ -36,8 +36,8 @@ FLAGS = [
     "-I", CSRC, "-I", INCLUDE,
 ]
 N_EPI = 11
-FP8_KERNELS = ["fp8_gemm", "fp8_quantize", "experts"]
-HOST_SOURCES = ["ep_api", "fp8_api"]
+FP8_KERNELS = ["fp8_gemm", "fp8_quantize", "experts", "fp8_backward", "norm", "route"]
+HOST_SOURCES = ["ep_api", "fp8_api", "block_api"]
 REMARKS = ["-Rpass-analysis=kernel-resource-usage"]
 REPORT = os.path.join(BUILD, "resource_usage.json")
 
@@ -143,8 +143,8 @@ HOSTSAN_LIB = os.path.join(BUILD, "libep_hostsan.so")
 
 
 def build_host_sanitized(verbose=False):
-    """Host-sanitizer build of the C ABI for the CPU tests: ep_api.cpp and fp8_api.cpp (validation,
-    planning, dispatch; host code only) compiled by g++ with AddressSanitizer and UndefinedBehavior-
+    """Host-sanitizer build of the C ABI for the CPU tests: ep_api.cpp, fp8_api.cpp and block_api.cpp
+    (validation, planning, dispatch; host code only) compiled by g++ with AddressSanitizer and UndefinedBehavior-
     Sanitizer, linked with the kernel objects of the last build() (not instrumented).  Load it
     with EP_LIBRARY pointing here and the sanitizer runtimes in LD_PRELOAD."""
     objs = sorted(os.path.join(BUILD, f) for f in os.listdir(BUILD) if f.startswith("gemm_") and f.endswith(".o"))

@@ -1,0 +1,171 @@
+// C ABI of the root-mean-square norm, the routing to experts and the gradient of the 8-bit products' epilogue: validation
+// and dispatch.  Every call only enqueues kernels; workspaces are the caller's.
+#include "api_shared.hpp"
+#include "block_ops.hpp"
+
+#include <cmath>
+
+using namespace ep;
+
+namespace {
+
+constexpr int64_t kMaxFeatures = (int64_t)1 << 26;
+constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of a launch, fewer than
+
+// what the norm and its gradients check alike
+ep_status check_norm(int64_t m, int64_t h, int elt, const void* weight, int weight_elt) {
+  EP_REQUIRE(m >= 1 && h >= 1, EP_ERR_INVALID_ARG, "sizes must be at least 1");
+  EP_REQUIRE(m < kMaxCount && h < kMaxFeatures, EP_ERR_UNSUPPORTED, "rows must be below 2^31 - 4096, features below 2^26");
+  const ep_status st = check_elt(elt);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(weight, EP_ERR_INVALID_ARG, "null pointer");
+  EP_REQUIRE(weight_elt == elt || weight_elt == EP_ELT_F32, EP_ERR_UNSUPPORTED, "the weight must be fp32 or of x's type");
+  EP_REQUIRE(aligned(weight, elt_size(weight_elt)), EP_ERR_INVALID_ARG, "misaligned pointer");
+  EP_REQUIRE(norm_threads(m, h) < kMaxThreads, EP_ERR_UNSUPPORTED, "too many rows for one launch");
+  return EP_OK;
+}
+
+ep_status check_route(int64_t tokens, int64_t experts, int64_t topk, int elt, int score, double scale) {
+  EP_REQUIRE(tokens >= 0 && experts >= 1 && topk >= 1, EP_ERR_INVALID_ARG, "sizes must be at least 1 (tokens: 0)");
+  EP_REQUIRE(tokens <= (int64_t)1 << 25, EP_ERR_UNSUPPORTED, "too many tokens for one launch");
+  EP_REQUIRE(experts <= kRouteExperts && topk <= kRouteChoices, EP_ERR_UNSUPPORTED, "at most %d experts and %d choices", kRouteExperts,
+             kRouteChoices);
+  EP_REQUIRE(topk <= experts, EP_ERR_INVALID_ARG, "more choices than experts");
+  EP_REQUIRE(score == SC_SOFTMAX || score == SC_SIGMOID, EP_ERR_UNSUPPORTED, "unknown score %d", score);
+  EP_REQUIRE(std::isfinite(scale), EP_ERR_INVALID_ARG, "the scale must be finite");
+  return check_elt(elt);
+}
+
+}  // namespace
+
+extern "C" {
+
+ep_status ep_rms_norm(const void* x, int64_t m, int64_t h, int64_t ldx, int elt, const void* residual, int64_t ld_res,
+                      const void* weight, int weight_elt, double eps, void* sum, int64_t ld_sum, void* y, int64_t ldy, float* scale,
+                      float* rstd, void* stream) {
+  api_clear();
+  ep_status st = check_norm(m, h, elt, weight, weight_elt);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(x && y && rstd && (!residual || sum), EP_ERR_INVALID_ARG, "null pointer");
+  const size_t size = elt_size(elt);
+  EP_REQUIRE(aligned(x, size) && aligned(residual, size) && aligned(sum, size) && aligned(y, scale ? 1 : size) && aligned(scale, 4) &&
+                 aligned(rstd, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
+  EP_REQUIRE(ldx >= h && ldy >= h && (!residual || (ld_res >= h && ld_sum >= h)), EP_ERR_INVALID_ARG, "row stride below the row length");
+  EP_REQUIRE(eps >= 0.0 && std::isfinite((float)eps), EP_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  NormArgs p{};
+  p.x = x; p.res = residual; p.w = weight; p.sum = sum; p.y = y; p.scale = scale; p.rstd = rstd;
+  p.ldx = ldx; p.ld_res = ld_res; p.ld_sum = ld_sum; p.ldy = ldy;
+  p.eps = (float)eps; p.m = (int)m; p.h = (int)h; p.w32 = weight_elt == EP_ELT_F32;
+  return done(launch_rms_norm(elt, p, (hipStream_t)stream), "rms_norm");
+}
+
+ep_status ep_rms_norm_backward_workspace(int64_t m, int64_t h, size_t* bytes) {
+  api_clear();
+  EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
+  *bytes = 0;
+  if (m >= 1 && h >= 1 && m < kMaxCount && h < kMaxFeatures) *bytes = (size_t)norm_back_strips(m, h) * h * 4;
+  return EP_OK;
+}
+
+ep_status ep_rms_norm_backward(const void* dy, int64_t m, int64_t h, int64_t ld_dy, int elt, const void* x, int64_t ldx,
+                               const void* weight, int weight_elt, const float* rstd, const void* dresidual, int64_t ld_dres,
+                               void* dx, int64_t ld_dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  api_clear();
+  ep_status st = check_norm(m, h, elt, weight, weight_elt);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(dy && x && rstd && dx && dweight, EP_ERR_INVALID_ARG, "null pointer");
+  const size_t size = elt_size(elt);
+  EP_REQUIRE(aligned(dy, size) && aligned(x, size) && aligned(dresidual, size) && aligned(dx, size) && aligned(rstd, 4) &&
+                 aligned(dweight, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
+  EP_REQUIRE(ld_dy >= h && ldx >= h && ld_dx >= h && (!dresidual || ld_dres >= h), EP_ERR_INVALID_ARG, "row stride below the row length");
+  const int strips = norm_back_strips(m, h);
+  EP_REQUIRE(workspace && workspace_bytes >= (size_t)strips * h * 4 && aligned(workspace, 16), EP_ERR_INVALID_ARG,
+             "the workspace is not 16-byte aligned or smaller than ep_rms_norm_backward_workspace says");
+  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  NormBackArgs p{};
+  p.dy = dy; p.x = x; p.w = weight; p.rstd = rstd; p.dres = dresidual; p.dx = dx; p.dw = dweight; p.part = (float*)workspace;
+  p.ld_dy = ld_dy; p.ldx = ldx; p.ld_dres = ld_dres; p.ld_dx = ld_dx;
+  p.m = (int)m; p.h = (int)h; p.w32 = weight_elt == EP_ELT_F32; p.strips = strips;
+  return done(launch_rms_norm_backward(elt, p, (hipStream_t)stream), "rms_norm_backward");
+}
+
+ep_status ep_expert_route(const void* logits, int64_t tokens, int64_t experts, int64_t ld, int elt, const float* bias, int score,
+                          int64_t groups, int64_t topk_groups, int group_top, int64_t topk, int renormalize, double scale,
+                          int32_t* ids, float* weights, void* stream) {
+  api_clear();
+  ep_status st = check_route(tokens, experts, topk, elt, score, scale);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(tokens == 0 || (logits && ids && weights), EP_ERR_INVALID_ARG, "null pointer");
+  EP_REQUIRE(aligned(logits, elt_size(elt)) && aligned(bias, 4) && aligned(ids, 4) && aligned(weights, 4), EP_ERR_INVALID_ARG,
+             "misaligned pointer");
+  EP_REQUIRE(ld >= experts, EP_ERR_INVALID_ARG, "row stride below the row length");
+  EP_REQUIRE(groups >= 1 && topk_groups >= 1 && topk_groups <= groups, EP_ERR_INVALID_ARG, "between 1 and all of the groups are kept");
+  EP_REQUIRE(groups <= 64, EP_ERR_UNSUPPORTED, "at most 64 groups");
+  EP_REQUIRE(experts % groups == 0, EP_ERR_INVALID_ARG, "the groups must divide the experts");
+  EP_REQUIRE(topk <= topk_groups * (experts / groups), EP_ERR_INVALID_ARG, "more choices than experts in the groups that are kept");
+  EP_REQUIRE(group_top == 1 || group_top == 2, EP_ERR_UNSUPPORTED, "a group's score is of its highest key or its two highest");
+  if (tokens == 0) return EP_OK;
+  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  RouteArgs p{};
+  p.logits = logits; p.bias = bias; p.ids = ids; p.weights = weights; p.ld = ld;
+  p.tokens = (int)tokens; p.experts = (int)experts; p.topk = (int)topk; p.score = score;
+  p.groups = (int)groups; p.topk_groups = (int)topk_groups; p.group_top = group_top; p.renormalize = renormalize != 0; p.scale = scale;
+  return done(launch_route(elt, p, (hipStream_t)stream), "expert_route");
+}
+
+ep_status ep_expert_route_backward(const float* dweights, int64_t ld_dw, int64_t tokens, int64_t topk, const void* logits,
+                                   int64_t experts, int64_t ld, int elt, const int32_t* ids, int score, int renormalize, double scale,
+                                   void* dlogits, int64_t ld_out, void* stream) {
+  api_clear();
+  ep_status st = check_route(tokens, experts, topk, elt, score, scale);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(tokens == 0 || (dweights && logits && ids && dlogits), EP_ERR_INVALID_ARG, "null pointer");
+  EP_REQUIRE(aligned(logits, elt_size(elt)) && aligned(dlogits, elt_size(elt)) && aligned(dweights, 4) && aligned(ids, 4),
+             EP_ERR_INVALID_ARG, "misaligned pointer");
+  EP_REQUIRE(ld >= experts && ld_out >= experts && ld_dw >= topk, EP_ERR_INVALID_ARG, "row stride below the row length");
+  if (tokens == 0) return EP_OK;
+  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  RouteBackArgs p{};
+  p.logits = logits; p.ids = ids; p.dweights = dweights; p.dlogits = dlogits;
+  p.ld = ld; p.ld_dw = ld_dw; p.ld_out = ld_out;
+  p.tokens = (int)tokens; p.experts = (int)experts; p.topk = (int)topk; p.score = score; p.renormalize = renormalize != 0; p.scale = scale;
+  return done(launch_route_backward(elt, p, (hipStream_t)stream), "expert_route_backward");
+}
+
+ep_status ep_epilogue_backward_fp8_workspace(int64_t m, int64_t n, size_t* bytes) {
+  api_clear();
+  EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
+  *bytes = 0;
+  if (m >= 1 && n >= 1 && m < kMaxCount && n < kMaxCount) *bytes = (size_t)((m + kScaleBlock - 1) / kScaleBlock) * n * 4;
+  return EP_OK;
+}
+
+ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64_t ld, int elt, int activation, const void* pre,
+                                   int64_t ld_pre, void* q, int64_t ldq, float* scale, void* q_t, int64_t ldq_t, float* scale_t,
+                                   float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  api_clear();
+  EP_REQUIRE(m >= 1 && n >= 1, EP_ERR_INVALID_ARG, "sizes must be at least 1");
+  EP_REQUIRE(m < kMaxCount && n < kMaxCount, EP_ERR_UNSUPPORTED, "sizes must be below 2^31 - 4096");
+  ep_status st = check_elt(elt);
+  if (st != EP_OK) return st;
+  EP_REQUIRE(activation >= ACT_NONE && activation <= ACT_SILU, EP_ERR_UNSUPPORTED, "unknown activation %d", activation);
+  EP_REQUIRE(dout && q && scale && q_t && scale_t && dbias, EP_ERR_INVALID_ARG, "null pointer");
+  EP_REQUIRE((pre != nullptr) == (activation != ACT_NONE), EP_ERR_INVALID_ARG, "an activation's gradient needs its pre-activation, no other does");
+  EP_REQUIRE(aligned(dout, elt_size(elt)) && aligned(pre, elt_size(elt)) && aligned(scale, 4) && aligned(scale_t, 4) && aligned(dbias, 4),
+             EP_ERR_INVALID_ARG, "misaligned pointer");
+  EP_REQUIRE(ld >= n && (!pre || ld_pre >= n) && ldq >= n && ldq_t >= m, EP_ERR_INVALID_ARG, "row stride below the row length");
+  const int64_t blocks = (m + kScaleBlock - 1) / kScaleBlock;
+  EP_REQUIRE(blocks * ((n + kScaleBlock - 1) / kScaleBlock) < ((int64_t)1 << 24), EP_ERR_UNSUPPORTED, "the matrix has too many blocks for one launch");
+  EP_REQUIRE(workspace && workspace_bytes >= (size_t)blocks * n * 4 && aligned(workspace, 16), EP_ERR_INVALID_ARG,
+             "the workspace is not 16-byte aligned or smaller than ep_epilogue_backward_fp8_workspace says");
+  if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
+  EpilogBackArgs p{};
+  p.dout = dout; p.pre = pre; p.ld = ld; p.ldp = ld_pre; p.m = (int)m; p.n = (int)n; p.act = activation;
+  p.q = (uint8_t*)q; p.scale = scale; p.qt = (uint8_t*)q_t; p.scale_t = scale_t; p.ldq = ldq; p.ldqt = ldq_t; p.part = (float*)workspace;
+  const hipError_t e = launch_epilogue_backward(elt, p, (hipStream_t)stream);
+  if (e != hipSuccess) return done(e, "epilogue_backward_fp8");
+  return done(launch_column_sums(p.part, (int)blocks, n, (int)n, dbias, (hipStream_t)stream), "epilogue_backward_fp8");
+}
+
+}  // extern "C"

@@ -1,0 +1,87 @@
+// Interface between the C ABI of the norm, the expert routing and the 8-bit products' epilogue gradients (block_api.cpp)
+// and their kernels (norm.hip, route.hip, fp8_backward.hip).
+#pragma once
+#include "fp8_ops.hpp"
+
+namespace ep {
+
+struct NormArgs {
+  const void* x;                     // [m][h]
+  const void* res;                   // [m][h] added to x, or null
+  const void* w;                     // [h]
+  void* sum;                         // [m][h] x + res rounded (with res only)
+  void* y;                           // [m][h] of x's type, or e4m3
+  float* scale;                      // quantised: [ceil(h / 128)][m]
+  float* rstd;                       // [m]
+  int64_t ldx, ld_res, ld_sum, ldy;
+  float eps;
+  int m, h;
+  int w32;                           // w is fp32 and x is not
+};
+// threads of a launch, at most: rows of up to 512 values take 16 or 64 lanes each, others a workgroup
+constexpr int64_t norm_threads(int64_t m, int64_t h) { return h <= 128 ? (m + 15) / 16 * 256 : h <= 512 ? (m + 3) / 4 * 256 : m * 1024; }
+hipError_t launch_rms_norm(int elt, const NormArgs& p, hipStream_t s);
+
+struct NormBackArgs {
+  const void* dy;                    // [m][h]
+  const void* x;                     // [m][h], what was normalised
+  const void* w;                     // [h]
+  const float* rstd;                 // [m]
+  const void* dres;                  // [m][h] added to dx, or null
+  void* dx;                          // [m][h]
+  float* dw;                         // [h]
+  float* part;                       // [strips][h]
+  int64_t ld_dy, ldx, ld_dres, ld_dx;
+  int m, h;
+  int w32;
+  int strips;                        // workgroups the rows are dealt out to
+};
+int norm_back_strips(int64_t m, int64_t h);
+hipError_t launch_rms_norm_backward(int elt, const NormBackArgs& p, hipStream_t s);
+
+// out[c] = sum over rows of part[row][c], rows ld apart, in a fixed order
+hipError_t launch_column_sums(const float* part, int rows, int64_t ld, int cols, float* out, hipStream_t s);
+
+constexpr int kRouteExperts = 1024;  // at most
+constexpr int kRouteChoices = 64;
+enum Score : int { SC_SOFTMAX = 0, SC_SIGMOID = 1 };
+
+struct RouteArgs {
+  const void* logits;                // [T][E]
+  const float* bias;                 // [E], or null
+  int* ids;                          // [T][k]
+  float* weights;                    // [T][k]
+  int64_t ld;
+  int tokens, experts, topk;
+  int score, groups, topk_groups, group_top, renormalize;
+  double scale;
+};
+hipError_t launch_route(int elt, const RouteArgs& p, hipStream_t s);
+
+struct RouteBackArgs {
+  const void* logits;                // [T][E]
+  const int* ids;                    // [T][k]
+  const float* dweights;             // [T][k]
+  void* dlogits;                     // [T][E]
+  int64_t ld, ld_dw, ld_out;
+  int tokens, experts, topk;
+  int score, renormalize;
+  double scale;
+};
+hipError_t launch_route_backward(int elt, const RouteBackArgs& p, hipStream_t s);
+
+struct EpilogBackArgs {
+  const void* dout;                  // [m][n]
+  const void* pre;                   // [m][n], or null: no activation
+  int64_t ld, ldp;
+  int m, n, act;
+  uint8_t* q;                        // [m][n] e4m3, scales [ceil(n / 128)][m]
+  float* scale;
+  uint8_t* qt;                       // [n][m] e4m3, scales [ceil(m / 128)][n]
+  float* scale_t;
+  int64_t ldq, ldqt;
+  float* part;                       // [ceil(m / 128)][n] column sums of row blocks
+};
+hipError_t launch_epilogue_backward(int elt, const EpilogBackArgs& p, hipStream_t s);
+
+}  // namespace ep

@@ -1,31 +1,13 @@
 // C ABI of the 8-bit block-scaled products and the expert operators: validation and dispatch.  Every
 // call only enqueues kernels; workspaces are the caller's.
-#include "ep.h"
 #include "api_shared.hpp"
-#include "fp8_ops.hpp"
 
 using namespace ep;
 
 namespace {
 
 constexpr int64_t kMaxLd8 = (int64_t)1 << 23;  // 256 rows stay inside one 2^31-byte buffer window
-constexpr int64_t kMaxCount = ((int64_t)1 << 31) - 4096;
 constexpr int64_t kMaxScaleStride = (int64_t)1 << 21;  // as are 256 rows' scales
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-ep_status done(hipError_t e, const char* what) {
-  if (e != hipSuccess) return (ep_status)api_fail(EP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return EP_OK;
-}
-#define EP_REQUIRE(cond, status, ...) \
-  do {                                \
-    if (!(cond)) return (ep_status)api_fail(status, __VA_ARGS__); \
-  } while (0)
-
-ep_status check_elt(int elt) {
-  EP_REQUIRE(elt == EP_ELT_F16 || elt == EP_ELT_BF16 || elt == EP_ELT_F32, EP_ERR_UNSUPPORTED, "unknown element type %d", elt);
-  return EP_OK;
-}
 
 // what the three products check alike; `rows_a` and `rows_b` are the operands' row counts, k their length
 ep_status check_product(int64_t rows_a, int64_t rows_b, int64_t k, const void* a, int64_t lda, const float* sa,
@@ -72,6 +54,41 @@ constexpr int64_t kRowsColumns = ((int64_t)1 << 28) - 16;
 bool few_rows(int64_t rows, int64_t n, int64_t experts) { return rows <= 4 * experts && n <= kRowsColumns; }
 bool few_rows(int64_t rows, int64_t n) { return rows <= kRowsPath && n <= kRowsColumns; }
 
+// the plain product, with an epilogue or without
+ep_status matmul(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m, int64_t sa_k,
+                 const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d, int64_t ldd, int out,
+                 void* workspace, size_t workspace_bytes, void* stream, const Fp8Epilog* epilog) {
+  api_clear();
+  ep_status st = check_product(m, n, k, a, lda, sa, sa_m, sa_k, b, ldb, sb, sb_n, sb_k, d, ldd, n, out);
+  if (st != EP_OK) return st;
+  Fp8GemmEpilog p{};
+  p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;
+  p.lda = lda; p.ldb = ldb; p.ldd = ldd;
+  p.sa_m = sa_m; p.sa_k = sa_k; p.sb_n = sb_n; p.sb_k = sb_k;
+  p.M = (int)m; p.N = (int)n; p.K = (int)k;
+  p.splits = 1;
+  p.kb_per_split = (int)((k + 127) / 128);
+  const bool rows = few_rows(m, n);
+  if (!rows) {
+    if ((st = check_tiles(tiles_of(m), tiles_of(n), 1)) != EP_OK) return st;
+    p.splits = fp8_splits(p.M, p.N, p.K);
+    if (p.splits > 1) {
+      EP_REQUIRE(workspace && workspace_bytes >= (size_t)p.splits * m * n * 4, EP_ERR_INVALID_ARG,
+                 "the workspace is smaller than ep_matmul_fp8_workspace says");
+      EP_REQUIRE(aligned(workspace, 16), EP_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
+      p.kb_per_split = (p.kb_per_split + p.splits - 1) / p.splits;
+      p.part = (float*)workspace;
+    }
+  }
+  if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
+  if (epilog) {
+    p.e = *epilog;
+    return done(launch_fp8_epilog(out, rows, p, (hipStream_t)stream), "matmul_fp8_epilog");
+  }
+  if (rows) return done(launch_fp8_rows(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
+  return done(launch_fp8_tiles(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
+}
+
 }  // namespace
 
 extern "C" {
@@ -107,31 +124,25 @@ ep_status ep_matmul_fp8_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes
 ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m,
                         int64_t sa_k, const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d,
                         int64_t ldd, int out, void* workspace, size_t workspace_bytes, void* stream) {
+  return matmul(m, n, k, a, lda, sa, sa_m, sa_k, b, ldb, sb, sb_n, sb_k, d, ldd, out, workspace, workspace_bytes, stream, nullptr);
+}
+
+ep_status ep_matmul_fp8_epilog(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m,
+                               int64_t sa_k, const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d,
+                               int64_t ldd, int out, const void* bias, int bias_elt, int activation, const void* residual,
+                               int64_t ld_res, void* pre, int64_t ld_pre, void* workspace, size_t workspace_bytes, void* stream) {
   api_clear();
-  ep_status st = check_product(m, n, k, a, lda, sa, sa_m, sa_k, b, ldb, sb, sb_n, sb_k, d, ldd, n, out);
+  const ep_status st = check_elt(out);
   if (st != EP_OK) return st;
-  Fp8Gemm p{};
-  p.a = (const uint8_t*)a; p.b = (const uint8_t*)b; p.sa = sa; p.sb = sb; p.d = d;
-  p.lda = lda; p.ldb = ldb; p.ldd = ldd;
-  p.sa_m = sa_m; p.sa_k = sa_k; p.sb_n = sb_n; p.sb_k = sb_k;
-  p.M = (int)m; p.N = (int)n; p.K = (int)k;
-  p.splits = 1;
-  p.kb_per_split = (int)((k + 127) / 128);
-  const bool rows = few_rows(m, n);
-  if (!rows) {
-    if ((st = check_tiles(tiles_of(m), tiles_of(n), 1)) != EP_OK) return st;
-    p.splits = fp8_splits(p.M, p.N, p.K);
-    if (p.splits > 1) {
-      EP_REQUIRE(workspace && workspace_bytes >= (size_t)p.splits * m * n * 4, EP_ERR_INVALID_ARG,
-                 "the workspace is smaller than ep_matmul_fp8_workspace says");
-      EP_REQUIRE(aligned(workspace, 16), EP_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
-      p.kb_per_split = (p.kb_per_split + p.splits - 1) / p.splits;
-      p.part = (float*)workspace;
-    }
-  }
-  if ((st = (ep_status)api_stream(stream, &p.cus)) != EP_OK) return st;
-  if (rows) return done(launch_fp8_rows(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
-  return done(launch_fp8_tiles(GM_MATMUL, out, p, (hipStream_t)stream), "matmul_fp8");
+  EP_REQUIRE(activation >= ACT_NONE && activation <= ACT_SILU, EP_ERR_UNSUPPORTED, "unknown activation %d", activation);
+  EP_REQUIRE(!bias || bias_elt == out || bias_elt == EP_ELT_F32, EP_ERR_UNSUPPORTED, "the bias must be fp32 or of the output's type");
+  EP_REQUIRE(aligned(bias, bias ? elt_size(bias_elt) : 1) && aligned(residual, elt_size(out)) && aligned(pre, elt_size(out)),
+             EP_ERR_INVALID_ARG, "misaligned bias, residual or pre-activation");
+  EP_REQUIRE((!residual || ld_res >= n) && (!pre || ld_pre >= n), EP_ERR_INVALID_ARG,
+             "row stride of the residual or the pre-activation below the row length");
+  EP_REQUIRE(!residual || ld_res < kMaxLd8, EP_ERR_UNSUPPORTED, "the residual's row stride must be below 2^23");  // (as an operand's)
+  const Fp8Epilog e{bias, residual, pre, ld_res, ld_pre, activation, bias_elt == EP_ELT_F32};
+  return matmul(m, n, k, a, lda, sa, sa_m, sa_k, b, ldb, sb, sb_n, sb_k, d, ldd, out, workspace, workspace_bytes, stream, &e);
 }
 
 ep_status ep_grouped_matmul_fp8(int64_t rows, int64_t n, int64_t k, int64_t experts, const int32_t* offsets, const void* a,

@@ -125,6 +125,50 @@ __device__ __forceinline__ void store8(char* p, int n, const float* f) {
     if (i < n) store_elt<E>(p + i * elt_size(E), f[i]);
 }
 
+// 8 neighbouring values of a row of `len` >= 8 at column n, wherever the row ends: near its end the last 8 are loaded and
+// moved down, without branches.  What lies at or past the end is undefined.
+template <int N>
+__device__ __forceinline__ void move_down(uint32_t (&w)[N], int by) {  // by whole words, up to N - 1
+#pragma unroll
+  for (int d = 1; d < N; d *= 2) {
+    uint32_t on = by & d ? ~0u : 0u;
+    asm("" : "+v"(on));  // (bits, not a condition: those are short of scalar registers)
+#pragma unroll
+    for (int i = 0; i + d < N; ++i) w[i] = (w[i + d] & on) | (w[i] & ~on);
+  }
+}
+__device__ __forceinline__ u32x4 window8_16(const char* row, int n, int len) {  // of 16-bit values, as they are
+  const int at = min(n, len - 8);
+  const u32x4 v = *(const u32x4_u*)(row + (uint32_t)at * 2u);
+  if (len % 8 == 0) return v;
+  const int by = n - at;
+  uint32_t w[4] = {v[0], v[1], v[2], v[3]};
+  move_down<4>(w, by >> 1);
+  if (len & 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = by & 1 ? (w[i] >> 16) | (i < 3 ? w[i + 1] << 16 : 0u) : w[i];
+  }
+  return u32x4{w[0], w[1], w[2], w[3]};
+}
+template <int E>
+__device__ __forceinline__ void window8(const char* row, int n, int len, float* f) {
+  if constexpr (E == EL_F32) {
+    const int at = min(n, len - 8);
+    const u32x4 a = *(const u32x4_u*)(row + (int64_t)at * 4), b = *(const u32x4_u*)(row + (int64_t)at * 4 + 16);
+    uint32_t w[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    if (len % 8) move_down<8>(w, n - at);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = elt_f32<E>(w[i]);
+  } else {
+    const u32x4 w = window8_16(row, n, len);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = elt_f32<E>(w[i] & 0xffffu);
+      f[2 * i + 1] = elt_f32<E>(w[i] >> 16);
+    }
+  }
+}
+
 // |v| of a finite value, 0 of an infinity or NaN
 __device__ __forceinline__ float finite_abs(float v) {
   const float a = __builtin_fabsf(v);

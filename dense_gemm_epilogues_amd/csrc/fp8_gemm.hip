@@ -20,7 +20,9 @@
 // e4m3 value, and multiplied by v_mfma_f32_16x16x32_f16, whose sums are fp32 throughout: fp32 outputs and, but for
 // weight gradients, sums of at most 256 values (fp8_wide_kernel; the latter bound by the output's bytes), and the
 // few-row kernel (bound by the weights').
-#include "fp8_device.hpp"
+#include <type_traits>
+
+#include "fp8_epilog.hpp"
 
 namespace ep {
 namespace {
@@ -145,23 +147,29 @@ __device__ __forceinline__ T* global_ptr(T* p) {
 }
 
 // A kernel's only argument, read from its segment here and not kept in registers from before a loop.
-__device__ __forceinline__ Fp8Gemm args_here() {
+template <class Args = Fp8Gemm>
+__device__ __forceinline__ Args args_here() {
   typedef const __attribute__((address_space(4))) uint32_t* Words;
   const uint64_t at = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
   uint32_t lo = (uint32_t)at, hi = (uint32_t)(at >> 32);
   asm volatile("" : "+s"(lo), "+s"(hi));
   const Words k = (Words)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)hi) << 32 |
                           (uint32_t)__builtin_amdgcn_readfirstlane((int)lo));
-  uint32_t w[sizeof(Fp8Gemm) / 4];
+  uint32_t w[sizeof(Args) / 4];
 #pragma unroll
-  for (size_t i = 0; i < sizeof(Fp8Gemm) / 4; ++i) w[i] = k[i];
-  Fp8Gemm p = __builtin_bit_cast(Fp8Gemm, w);
+  for (size_t i = 0; i < sizeof(Args) / 4; ++i) w[i] = k[i];
+  Args p = __builtin_bit_cast(Args, w);
   // (global, which the compiler can no longer see; flat accesses would count as LDS accesses too, and with
   // those pending it waits for all fragment reads at once)
   p.sa = global_ptr(p.sa);
   p.sb = global_ptr(p.sb);
   p.d = global_ptr(p.d);
   p.offsets = global_ptr(p.offsets);
+  if constexpr (!std::is_same_v<Args, Fp8Gemm>) {
+    p.e.bias = global_ptr(p.e.bias);
+    p.e.res = global_ptr(p.e.res);
+    p.e.pre = global_ptr(p.e.pre);
+  }
   return p;
 }
 
@@ -333,6 +341,30 @@ __device__ __forceinline__ void store_tile(const Fp8Gemm& p, const Tile& t, int 
   }
 }
 
+// 64 columns of 16 rows in 16-bit values: a and b are a lane's 8 of its row's first and second 32, which neighbouring
+// lanes trade, so that one store writes whole lines of the even lanes' rows (at d, `rows` of them and the odd lanes'
+// inside the matrix), the other of the odd lanes'
+__device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int left, bool odd, u32x4 a, u32x4 b) {
+  u32x4 x, y;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
+    x[h] = odd ? got : a[h];
+    y[h] = odd ? b[h] : got;
+  }
+  if (left >= 8) {
+    if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)d);
+    if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(d + ld * 2));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= left) continue;
+      if (rows > 0) *(uint16_t*)(d + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+      if (rows > 1) *(uint16_t*)(d + ld * 2 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
 // The same for 16-bit outputs and rows in row_in's order: neighbouring lanes, which hold neighbouring rows,
 // first trade halves of 64 columns, so that a store instruction writes whole 128-byte lines, which leave the
 // caches to the operands (non-temporal).  The experts' weight gradients, 2.7 GB of stores: 1518 us with half
@@ -350,27 +382,129 @@ __device__ __forceinline__ void store_lines(const Fp8Gemm& p, const Tile& t, int
     const int rows = t.mv - m_at - m;
 #pragma unroll
     for (int j = 0; j < NT; j += 4) {
-      u32x4 a, b, x, y;  // the row's first and second 32 columns' pieces; traded
+      u32x4 a, b;  // the row's first and second 32 columns' pieces
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         a[h] = pack2_elt<OT>(acc[i][j + h / 2][2 * (h & 1)], acc[i][j + h / 2][2 * (h & 1) + 1]);
         b[h] = pack2_elt<OT>(acc[i][j + 2 + h / 2][2 * (h & 1)], acc[i][j + 2 + h / 2][2 * (h & 1) + 1]);
-        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
-        x[h] = odd ? got : a[h];
-        y[h] = odd ? b[h] : got;
       }
-      const int left = t.nv - n_at - n0 - j * 16;
-      if (left >= 8) {
-        if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)(row + j * 32));
-        if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(row + p.ldd * 2 + j * 32));
-      } else {
+      store_pair(row + j * 32, p.ldd, rows, t.nv - n_at - n0 - j * 16, odd, a, b);
+    }
+  }
+}
+
+// Fewer than 8 columns, with an epilogue (a type of its own, which chooses finish_narrow: in the same kernel it
+// takes registers from finish_lines): they lie in one place of 16 lanes
+struct Fp8GemmNarrow : Fp8GemmEpilog {};
+template <int OT, int MT, int NT>
+__device__ __forceinline__ void finish_narrow(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
+  const int lane = here(lane_id());
+  if (n_at + (lane >> 4) > 0) return;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (e >= left) continue;
-          if (rows > 0) *(uint16_t*)(row + j * 32 + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
-          if (rows > 1) *(uint16_t*)(row + p.ldd * 2 + j * 32 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+  for (int i = 0; i < MT; ++i) {
+    const int m = m_at + row_in(i, lane & 15);
+    if (m >= t.mv) continue;
+    const int64_t row = t.m0 + m;
+#pragma unroll
+    for (int n = 0; n < 8; ++n)
+      if (n < t.nv) store_elt<OT>((char*)p.d + (row * p.ldd + n) * elt_size(OT), finish1<OT>(p.e, row, n, acc[i][n / 4][n & 3]));
+  }
+}
+
+// ---- with an epilogue: as store_tile and store_lines do, 64 (32) columns at a time for all rows, so that their bias
+// is read once
+template <int OT, int MT, int NT>
+__device__ __forceinline__ void finish_tile(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
+  const int lane = here(lane_id());
+  char* d = tile_d<GM_MATMUL, OT>(p, t);
+#pragma unroll
+  for (int j = 0; j < NT; j += 2) {
+    const int n = n_at + 8 * (lane >> 4) + j * 16, left = t.nv - n;
+    float bias[8];
+    load_bias8<OT>(p.e, t.n0 + n, left, bias);
+    if (left <= 0) continue;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = m_at + i * 16 + (lane & 15);
+      if (m >= t.mv) continue;
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = acc[i][j + e / 4][e & 3] + bias[e];
+      const int64_t row = t.m0 + m;
+      if (p.e.pre) store8<OT>((char*)p.e.pre + (row * p.e.ld_pre + t.n0 + n) * elt_size(OT), left, f);
+      finish8<OT>(p.e, row, t.n0 + n, left, f);
+      store8<OT>(d + (m * p.ldd + n) * elt_size(OT), left, f);
+    }
+  }
+}
+
+// the bias is in the accumulators from the start (start_bias); at least 8 columns
+template <int OT, int MT, int NT>
+__device__ __forceinline__ void finish_lines(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
+  const int lane = here(lane_id());
+  const bool odd = lane & 1;
+  const int own0 = n_at + 8 * (lane >> 4), n0 = own0 + (odd ? 32 : 0);
+  constexpr int UNITS = MT * NT / 4;  // 64 columns of 16 rows
+  u32x4 res[2][2];
+  const char* const res_at = (const char*)p.e.res + (int64_t)t.m0 * p.e.ld_res * 2;
+  auto load_res = [&](int x) __attribute__((always_inline)) {
+    const int i = x % MT, j = x / MT * 4;
+    const int own = min(m_at + row_in(i, lane & 15), t.mv - 1);  // (rows past the tile's read its last one)
+    const char* row = res_at + (uint32_t)(own * (int)p.e.ld_res) * 2u;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) res[x & 1][u] = window8_16(row, t.n0 + own0 + j * 16 + u * 32, p.N);
+  };
+  if (p.e.res) load_res(0);
+#pragma unroll
+  for (int x = 0; x < UNITS; ++x) {
+    const int i = x % MT, j = x / MT * 4;
+    if (p.e.res && x + 1 < UNITS) load_res(x + 1);
+    const int m = m_at + row_in(i, lane & 14), rows = t.mv - m;
+    const int n = n0 + j * 16, left = t.nv - n;
+    const int64_t row = t.m0 + m;
+    u32x4 out[2];
+    if (p.e.pre) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const f32x4 v = acc[i][j + 2 * u + h / 2];
+          out[u][h] = pack2_elt<OT>(v[2 * (h & 1)], v[2 * (h & 1) + 1]);
         }
+      store_pair((char*)p.e.pre + (row * p.e.ld_pre + t.n0 + n) * 2, p.e.ld_pre, rows, left, odd, out[0], out[1]);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = acc[i][j + 2 * u + e / 4][e & 3];
+      activate8(p.e.act, f);
+      if (p.e.res) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += elt_f32<OT>(e & 1 ? res[x & 1][u][e / 2] >> 16 : res[x & 1][u][e / 2] & 0xffffu);
       }
+#pragma unroll
+      for (int h = 0; h < 4; ++h) out[u][h] = pack2_elt<OT>(f[2 * h], f[2 * h + 1]);
+    }
+    store_pair((char*)p.d + (row * p.ldd + t.n0 + n) * 2, p.ldd, rows, left, odd, out[0], out[1]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// a wave's accumulators at a tile's start: the bias of their columns
+template <int OT, int MT, int NT>
+__device__ __forceinline__ void start_bias(const Fp8GemmEpilog& p, const Tile& t, int n_at, f32x4 (&acc)[MT][NT]) {
+  if (!p.e.bias) return;
+  const int n0 = t.n0 + n_at + 8 * (here(lane_id()) >> 4);
+#pragma unroll
+  for (int j = 0; j < NT; j += 2) {
+    float f[8];
+    if (p.e.bias32) window8<EL_F32>((const char*)p.e.bias, n0 + j * 16, p.N, f);
+    else window8<OT>((const char*)p.e.bias, n0 + j * 16, p.N, f);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      acc[i][j] = f32x4{f[0], f[1], f[2], f[3]};
+      acc[i][j + 1] = f32x4{f[4], f[5], f[6], f[7]};
     }
   }
 }
@@ -415,9 +549,9 @@ __device__ constexpr bool read_first(int j) {
 // one tile a workgroup, all loads at a step's start: 667).  What bounds it is power: the card runs it at 1.7 GHz of 2.4, the matrix unit is busy for 60 % of
 // the cycles.  From registers alone the same MFMAs with random operands reach 3863 TFLOP/s, 3484 with their
 // multiply-adds; without the loads (operands left in LDS) a step takes 12 % fewer cycles, without the multiply-adds 15 %.
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S>
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int S, class Args = Fp8Gemm>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
-void fp8_tile_kernel(Fp8Gemm p) {
+void fp8_tile_kernel(Args p) {
 #ifdef __HIP_DEVICE_COMPILE__  // (the host's pass drops a body with register constraints it does not know)
   constexpr int WAVES = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, MT = WTM / 16, NT = WTN / 16;
   constexpr int OPS = (BM + BN) * 128, STAGE = OPS + WAVES * 256;
@@ -433,7 +567,7 @@ void fp8_tile_kernel(Fp8Gemm p) {
 
   // the next tile with products, the others filled on the way
   auto next = [&](Tile& t) __attribute__((always_inline)) {
-    const Fp8Gemm q = args_here();
+    const Fp8Gemm q = args_here<Args>();
     t.nkb = 0;
     while (bid < tiles.count && t.nkb == 0) {
       t = tiles.at(q, xcd_order(bid, tiles.count));
@@ -459,7 +593,7 @@ void fp8_tile_kernel(Fp8Gemm p) {
   int64_t ls_step = 0;
   uint32_t lsoff;
   auto load_tile = [&](const Tile& t) __attribute__((always_inline)) {
-    const Fp8Gemm q = args_here();
+    const Fp8Gemm q = args_here<Args>();
     lda = (int)q.lda;
     ldb = (int)q.ldb;
     const int rows_a = t.mv - wave * 32, rows_b = t.nv - wave * 32;  // (at most 0: the wave loads zeros)
@@ -538,9 +672,14 @@ void fp8_tile_kernel(Fp8Gemm p) {
     t_last = 0.0f;
   };
 
+  auto start = [&](const Tile& t) __attribute__((always_inline)) {
+    if constexpr (std::is_same_v<Args, Fp8GemmEpilog>) start_bias<OT>(args_here<Args>(), t, wn * WTN, acc);
+  };
+
   Tile cur, ahead;
   if (!next(cur)) return;
   clear();
+  start(cur);
   load_tile(cur);
 #pragma unroll
   for (int s = 0; s < S; ++s) {
@@ -662,11 +801,14 @@ void fp8_tile_kernel(Fp8Gemm p) {
       // (the last loads write LDS too: not after the workgroup has left it)
       if (!more) __builtin_amdgcn_s_waitcnt(0x0070);
       add_last();
-      if constexpr (OT == EL_F32) store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
+      if constexpr (std::is_same_v<Args, Fp8GemmNarrow>) finish_narrow<OT>(args_here<Args>(), cur, wm * WTM, wn * WTN, acc);
+      else if constexpr (std::is_same_v<Args, Fp8GemmEpilog>) finish_lines<OT>(args_here<Args>(), cur, wm * WTM, wn * WTN, acc);
+      else if constexpr (OT == EL_F32) store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
       else store_lines<MODE, OT>(args_here(), cur, wm * WTM, wn * WTN, acc);
       done = !more;
       clear();
       cur = ahead;
+      if (more) start(cur);
       step = 0;
       steps = max(cur.nkb, S);
       on = steps_on();
@@ -677,9 +819,9 @@ void fp8_tile_kernel(Fp8Gemm p) {
 
 // ---- the same with operands widened to fp16: one tile a workgroup, 128 x 128 so that two of them share a
 // compute unit and one's loads pass behind the other's products.
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN>
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, class Args = Fp8Gemm>
 __global__ __launch_bounds__(64 * WGM * WGN) __attribute__((amdgpu_waves_per_eu(2)))
-void fp8_wide_kernel(Fp8Gemm p) {
+void fp8_wide_kernel(Args p) {
   constexpr int WAVES = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, MT = WTM / 16, NT = WTN / 16;
   constexpr int SLOTS = (BM + BN) / 8, PER_WAVE = SLOTS / WAVES, STAGE = (BM + BN) * 128;
   static_assert(SLOTS % WAVES == 0 && (BM / 8) % PER_WAVE == 0 && NT % 2 == 0 && WTN <= 128 && 128 % WTN == 0, "tile");
@@ -791,12 +933,14 @@ void fp8_wide_kernel(Fp8Gemm p) {
     }
   }
 
-  if (active) store_tile<MODE, OT, false>(p, tile, wm * WTM, wn * WTN, acc);
+  if (!active) return;
+  if constexpr (!std::is_same_v<Args, Fp8Gemm>) finish_tile<OT>(p, tile, wm * WTM, wn * WTN, acc);
+  else store_tile<MODE, OT, false>(p, tile, wm * WTM, wn * WTN, acc);
 }
 
 // D = sum of the K ranges' parts, in their order
-template <int OT>
-__global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm p) {
+template <int OT, class Args = Fp8Gemm>
+__global__ __launch_bounds__(256) void fp8_join_kernel(Args p) {
   const int64_t mn = (int64_t)p.M * p.N;
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8; i < mn; i += (int64_t)gridDim.x * 256 * 8) {
     float f[8], g[8];
@@ -810,12 +954,20 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm p) {
     const int64_t row = i / p.N, col = i - row * p.N;
     char* d = (char*)p.d;
     if (n == 8 && col + 8 <= p.N) {
+      if constexpr (!std::is_same_v<Args, Fp8Gemm>) {
+        load_bias8<OT>(p.e, (int)col, 8, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] += g[j];
+        if (p.e.pre) store8<OT>((char*)p.e.pre + (row * p.e.ld_pre + col) * elt_size(OT), 8, f);
+        finish8<OT>(p.e, row, (int)col, 8, f);
+      }
       store8<OT>(d + (row * p.ldd + col) * elt_size(OT), 8, f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (j >= n) continue;
         const int64_t r = (i + j) / p.N, c = i + j - r * p.N;
+        if constexpr (!std::is_same_v<Args, Fp8Gemm>) f[j] = finish1<OT>(p.e, r, (int)c, f[j]);
         store_elt<OT>(d + (r * p.ldd + c) * elt_size(OT), f[j]);
       }
     }
@@ -830,8 +982,8 @@ __global__ __launch_bounds__(256) void fp8_join_kernel(Fp8Gemm p) {
 // experts, n 4096, k 5120, in 30 us (5.5 TB/s, the inputs changing from pass to pass); the first form through LDS took
 // 32, through registers 40, with 8 waves a workgroup 35.
 constexpr int kRowsWaves = 4;
-template <int MODE, int OT>
-__global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Fp8Gemm p) {
+template <int MODE, int OT, class Args = Fp8Gemm>
+__global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Args p) {
   constexpr int NW = kRowsWaves, D = 3, AT_A = 2048, AT_S = AT_A + 1024, SLOT = AT_S + 256;  // 16 rows of b, 8 of a, 9 scales
   __shared__ __align__(128) char ring[NW * D * SLOT];  // (39 KB: four workgroups a compute unit)
   const int lane = lane_id(), wave = wave_id();
@@ -928,6 +1080,9 @@ __global__ __launch_bounds__(64 * kRowsWaves) void fp8_rows_kernel(Fp8Gemm p) {
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < NW; ++w) v += ((const float*)&red[w * 64 + (n >> 2) * 16 + m])[n & 3];
+      if constexpr (!std::is_same_v<Args, Fp8Gemm>) {
+        if (m < mv && n < nv) v = finish1<OT>(p.e, m0 + m, n0 + n, v);
+      }
       if (m < mv && n < nv) store_elt<OT>((char*)p.d + ((int64_t)(m0 + m) * p.ldd + n0 + n) * elt_size(OT), v);
     }
     __syncthreads();
@@ -944,23 +1099,23 @@ int64_t count_tiles(Fp8Gemm& p) {
 }
 
 // As many workgroups as run at once (a multiple of 8: a workgroup's tiles are all of one XCD's share).
-template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int PER_CU>
-hipError_t launch_tile(Fp8Gemm& p, hipStream_t s) {
+template <int MODE, int OT, int BM, int BN, int WGM, int WGN, int PER_CU, class Args>
+hipError_t launch_tile(Args& p, hipStream_t s) {
   const int64_t tiles = count_tiles<MODE, BM, BN>(p);
   const int whole = (p.cus >= 8 ? p.cus & ~7 : 8) * PER_CU;
-  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, 2><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
+  fp8_tile_kernel<MODE, OT, BM, BN, WGM, WGN, 2, Args><<<(unsigned)(tiles < whole ? tiles : whole), 64 * WGM * WGN, 0, s>>>(p);
   return hipGetLastError();
 }
 
-template <int MODE, int OT>
-hipError_t launch_wide(Fp8Gemm& p, hipStream_t s) {
+template <int MODE, int OT, class Args>
+hipError_t launch_wide(Args& p, hipStream_t s) {
   const int64_t tiles = count_tiles<MODE, 128, 128>(p);
-  fp8_wide_kernel<MODE, OT, 128, 128, 2, 2><<<(unsigned)tiles, 256, 0, s>>>(p);
+  fp8_wide_kernel<MODE, OT, 128, 128, 2, 2, Args><<<(unsigned)tiles, 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
-template <int MODE, int OT>
-hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
+template <int MODE, int OT, class Args>
+hipError_t launch_tiles(Args& p, hipStream_t s) {
   if constexpr (MODE == GM_MATMUL) {
     if (p.splits > 1) {
       Fp8Gemm q = p;
@@ -969,12 +1124,18 @@ hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
       const hipError_t e = OT == EL_F32 ? launch_wide<MODE, EL_F32>(q, s) : launch_tile<MODE, EL_F32, 128, 128, 2, 2, 2>(q, s);
       if (e != hipSuccess) return e;
       const int64_t b = ((int64_t)p.M * p.N + 2047) / 2048;
-      fp8_join_kernel<OT><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, s>>>(p);
+      fp8_join_kernel<OT, Args><<<(unsigned)(b < 4096 ? b : 4096), 256, 0, s>>>(p);
       return hipGetLastError();
     }
   }
   if constexpr (OT != EL_F32) {
     if (MODE == GM_WGRAD || p.K > 2 * kScaleBlock) {
+      if constexpr (std::is_same_v<Args, Fp8GemmEpilog>) {
+        if (p.N < 8) {
+          Fp8GemmNarrow q{p};
+          return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(q, s);
+        }
+      }
       // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 36 us
       // with operands that no cache holds, 59 with 80 large tiles); with more the large ones, which read half as much
       // through the caches (8192 x 17408 x 5120: 602 us, 744 with small ones)
@@ -987,11 +1148,11 @@ hipError_t launch_tiles(Fp8Gemm& p, hipStream_t s) {
   return launch_wide<MODE, OT>(p, s);
 }
 
-template <int MODE, int OT>
-hipError_t launch_rows(Fp8Gemm& p, hipStream_t s) {
+template <int MODE, int OT, class Args>
+hipError_t launch_rows(Args& p, hipStream_t s) {
   const unsigned groups = MODE == GM_GROUPED ? (unsigned)((p.experts < p.M ? p.experts : p.M) + 1) : 1u;
   const dim3 grid((unsigned)((p.N + 15) / 16), groups);
-  fp8_rows_kernel<MODE, OT><<<grid, 64 * kRowsWaves, 0, s>>>(p);
+  fp8_rows_kernel<MODE, OT, Args><<<grid, 64 * kRowsWaves, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -1034,6 +1195,12 @@ hipError_t launch_fp8_rows(int mode, int out, Fp8Gemm& p, hipStream_t s) {
   EP_CASE(GM_GROUPED, EL_F16) EP_CASE(GM_GROUPED, EL_BF16) EP_CASE(GM_GROUPED, EL_F32)
 #undef EP_CASE
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_fp8_epilog(int out, bool few, Fp8GemmEpilog& p, hipStream_t s) {
+  if (out == EL_F16) return few ? launch_rows<GM_MATMUL, EL_F16>(p, s) : launch_tiles<GM_MATMUL, EL_F16>(p, s);
+  if (out == EL_BF16) return few ? launch_rows<GM_MATMUL, EL_BF16>(p, s) : launch_tiles<GM_MATMUL, EL_BF16>(p, s);
+  return few ? launch_rows<GM_MATMUL, EL_F32>(p, s) : launch_tiles<GM_MATMUL, EL_F32>(p, s);
 }
 
 }  // namespace ep

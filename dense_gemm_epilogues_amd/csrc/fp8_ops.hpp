@@ -33,12 +33,28 @@ struct Fp8Gemm {
   int cus;                           // of the device
 };
 
+// what follows a product: P = a b^T + bias, D = act(P) + residual
+enum Activation : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_SILU = 3 };
+struct Fp8Epilog {
+  const void* bias;                  // [N], or null
+  const void* res;                   // [M][N] of D's type, or null
+  void* pre;                         // [M][N] of D's type: P, or null
+  int64_t ld_res, ld_pre;
+  int act;
+  int bias32;                        // bias is fp32, else of D's type
+};
+struct Fp8GemmEpilog : Fp8Gemm {
+  Fp8Epilog e;
+};
+
 enum GemmMode : int { GM_MATMUL = 0, GM_GROUPED = 1, GM_WGRAD = 2 };
 
 hipError_t launch_fp8_tiles(int mode, int out, Fp8Gemm& p, hipStream_t s);
 // few rows: b streams past them
 hipError_t launch_fp8_rows(int mode, int out, Fp8Gemm& p, hipStream_t s);
 int fp8_splits(int m, int n, int k);
+// the same of a plain product with an epilogue; few: a few rows
+hipError_t launch_fp8_epilog(int out, bool few, Fp8GemmEpilog& p, hipStream_t s);
 
 struct QuantArgs {
   const void* x;

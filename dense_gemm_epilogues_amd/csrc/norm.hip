@@ -1,0 +1,382 @@
+// Root-mean-square norm of rows, with the residual's addition before it and e4m3 rows with block scales behind it,
+// and its gradients.
+//
+//   r = round(x + res), rstd = (mean_j r_j^2 + eps)^-1/2, y_j = r_j rstd w_j
+//   dr_j = rstd (w_j dy_j - r_j rstd mean_k(w_k dy_k r_k rstd)) + dres_j,  dw_j = sum over rows of dy_j r_j rstd
+//
+// Everything is bound by HBM: a row is read once, held in registers as fp32 while its sum is made, and written once.
+// r is what later readers see (the residual stream, the backward pass), so the norm is of the rounded r.
+#include "block_ops.hpp"
+#include "fp8_device.hpp"
+
+namespace ep {
+namespace {
+
+constexpr int kMaxThreads = 1024;
+
+// sum over L neighbouring lanes, in every one of them
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < L; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// sum over the workgroup, in every thread; `red` holds a float for each wave and is free again behind the next barrier
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = lanes_sum<64>(v);
+  const int waves = (int)blockDim.x >> 6;
+  if (lane_id() == 0) red[wave_id()] = v;
+  __syncthreads();
+  float t = 0.0f;
+  for (int i = 0; i < waves; ++i) t += red[i];
+  return t;
+}
+
+template <int E>
+__device__ __forceinline__ float rounded(float v) {
+  if constexpr (E == EL_F32) return v;
+  else return elt_f32<E>(pack2_elt<E>(v, v) & 0xffffu);
+}
+
+// How a row's 8 values from column c on are reached.  ANY: rows of any length, with branches at the end; WHOLE: rows of a
+// multiple of 8 values; CUT: other rows of at least 8, without branches.
+enum Ends : int { ANY, WHOLE, CUT };
+template <int E, int ENDS>
+__device__ __forceinline__ void load_cols(const char* row, int c, int h, float* f) {
+  if constexpr (ENDS == ANY) {
+    load8<E>(row + (int64_t)c * elt_size(E), h - c, f);
+  } else {
+    window8<E>(row, ENDS == WHOLE ? min(c, h - 8) : c, ENDS == WHOLE ? h & ~7 : h, f);
+    if constexpr (ENDS == WHOLE) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = c < h ? f[i] : 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {  // (as bits: kept as truth values, eight of them take more scalar registers than there are)
+        int in = (i - (h - c)) >> 31;
+        asm("" : "+v"(in));
+        f[i] = __builtin_bit_cast(float, __builtin_bit_cast(int, f[i]) & in);
+      }
+    }
+  }
+}
+template <int E, int ENDS>
+__device__ __forceinline__ void store_cols(char* row, int c, int h, const float* f) {
+  if constexpr (ENDS == WHOLE) {
+    if (c < h) store8<E>(row + (int64_t)c * elt_size(E), 8, f);
+  } else {
+    int n = h - c;
+    if (ENDS == CUT) asm volatile("" : "+v"(n));  // (compared here, as above)
+    store8<E>(row + (int64_t)c * elt_size(E), n, f);
+  }
+}
+
+template <int E, int ENDS>
+__device__ __forceinline__ void load_weight(const void* w, int w32, int c, int h, float* f) {
+  if (E != EL_F32 && w32) load_cols<EL_F32, ENDS>((const char*)w, c, h, f);
+  else load_cols<E, ENDS>((const char*)w, c, h, f);
+}
+
+// 8 values of a row from column c on: x, or x + res rounded and written
+template <int E, bool RES, int ENDS>
+__device__ __forceinline__ void load_row(const NormArgs& p, int64_t row, int c, float* f) {
+  load_cols<E, ENDS>((const char*)p.x + row * p.ldx * elt_size(E), c, p.h, f);
+  if constexpr (RES) {
+    float g[8];
+    load_cols<E, ENDS>((const char*)p.res + row * p.ld_res * elt_size(E), c, p.h, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = rounded<E>(f[i] + g[i]);
+    store_cols<E, ENDS>((char*)p.sum + row * p.ld_sum * elt_size(E), c, p.h, f);
+  }
+}
+
+// y of 8 values; the 16 lanes of a scale block take part together
+template <int E, bool Q, int ENDS>
+__device__ __forceinline__ void store_y(const NormArgs& p, int64_t row, int c, float rstd, const float* f) {
+  const int n = p.h - c;
+  float w[8], y[8];
+  load_weight<E, ENDS>(p.w, p.w32, c, p.h, w);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = f[i] * rstd * w[i];
+  if constexpr (Q) {
+    float amax = kAmaxMin;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, finite_abs(y[i]));
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d));
+    if (n <= 0) return;
+    const float inv = scale_inv(amax);
+    const u32x2 q = {to_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                     to_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv)};
+    uint8_t* o = (uint8_t*)p.y + row * p.ldy + c;
+    if (ENDS == WHOLE || n >= 8) {
+      *(u32x2_u*)o = q;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < n) o[i] = (uint8_t)(q[i >> 2] >> (8 * (i & 3)));
+    }
+    if (c % kScaleBlock == 0) p.scale[(int64_t)(c / kScaleBlock) * p.m + row] = scale_of(amax);
+  } else {
+    store_cols<E, ENDS>((char*)p.y + row * p.ldy * elt_size(E), c, p.h, y);
+  }
+}
+
+__device__ __forceinline__ float rstd_of(float squares, int h, float eps) {
+  return 1.0f / __builtin_sqrtf(squares / (float)h + eps);
+}
+
+// Rows of at most 8 L values: L lanes each.
+template <int E, bool RES, bool Q, int L>
+__global__ __launch_bounds__(256) void norm_lanes_kernel(NormArgs p) {
+  const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  if (row >= p.m) return;
+  const int c = (int)(threadIdx.x % L) * 8;
+  float f[8];
+  load_row<E, RES, ANY>(p, row, c, f);
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += f[i] * f[i];
+  const float rstd = rstd_of(lanes_sum<L>(s), p.h, p.eps);
+  if (c == 0) p.rstd[row] = rstd;
+  store_y<E, Q, ANY>(p, row, c, rstd, f);
+}
+
+// A row a workgroup, CH times 8 values a thread.
+template <int E, bool RES, bool Q, int CH, int ENDS>
+__global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs p) {
+  __shared__ float red[kMaxThreads / 64];
+  const int64_t row = blockIdx.x;
+  const int step = (int)blockDim.x * 8;
+  float f[CH][8], s = 0.0f;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) load_row<E, RES, ENDS>(p, row, (int)threadIdx.x * 8 + k * step, f[k]);
+#pragma unroll
+  for (int k = 0; k < CH; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += f[k][i] * f[k][i];
+  const float rstd = rstd_of(block_sum(s, red), p.h, p.eps);
+  if (threadIdx.x == 0) p.rstd[row] = rstd;
+#pragma unroll
+  for (int k = 0; k < CH; ++k) store_y<E, Q, ENDS>(p, row, (int)threadIdx.x * 8 + k * step, rstd, f[k]);
+}
+
+// Rows too long for registers: read twice (r from where the thread itself has written it).
+template <int E, bool RES, bool Q>
+__global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs p) {
+  __shared__ float red[kMaxThreads / 64];
+  const int64_t row = blockIdx.x;
+  const int step = (int)blockDim.x * 8;
+  float f[8], s = 0.0f;
+  for (int c0 = 0; c0 < p.h; c0 += step) {
+    load_row<E, RES, ANY>(p, row, c0 + (int)threadIdx.x * 8, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += f[i] * f[i];
+  }
+  const float rstd = rstd_of(block_sum(s, red), p.h, p.eps);
+  if (threadIdx.x == 0) p.rstd[row] = rstd;
+  const char* r = RES ? (const char*)p.sum + row * p.ld_sum * elt_size(E) : (const char*)p.x + row * p.ldx * elt_size(E);
+  for (int c0 = 0; c0 < p.h; c0 += step) {
+    const int c = c0 + (int)threadIdx.x * 8;
+    load8<E>(r + (int64_t)c * elt_size(E), p.h - c, f);
+    store_y<E, Q, ANY>(p, row, c, rstd, f);
+  }
+}
+
+template <int E, bool RES, bool Q, int ENDS>
+void launch_norm_rows(const NormArgs& p, int lanes, hipStream_t s) {
+  const int threads = (lanes + 63) / 64 * 64;
+  if (threads <= kMaxThreads) norm_row_kernel<E, RES, Q, 1, ENDS><<<(unsigned)p.m, threads, 0, s>>>(p);
+  else if (lanes <= 2 * kMaxThreads) norm_row_kernel<E, RES, Q, 2, ENDS><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
+  else norm_row_kernel<E, RES, Q, 4, ENDS><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
+}
+
+template <int E, bool RES, bool Q>
+hipError_t launch_norm(const NormArgs& p, hipStream_t s) {
+  const int lanes = (p.h + 7) / 8;
+  if (lanes <= 16) norm_lanes_kernel<E, RES, Q, 16><<<(unsigned)((p.m + 15) / 16), 256, 0, s>>>(p);
+  else if (lanes <= 64) norm_lanes_kernel<E, RES, Q, 64><<<(unsigned)((p.m + 3) / 4), 256, 0, s>>>(p);
+  else if (lanes > 4 * kMaxThreads) norm_long_kernel<E, RES, Q><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
+  else if (p.h % 8 == 0) launch_norm_rows<E, RES, Q, WHOLE>(p, lanes, s);
+  else launch_norm_rows<E, RES, Q, CUT>(p, lanes, s);
+  return hipGetLastError();
+}
+
+template <int E>
+hipError_t launch_norm_e(const NormArgs& p, hipStream_t s) {
+  if (p.res) return p.scale ? launch_norm<E, true, true>(p, s) : launch_norm<E, true, false>(p, s);
+  return p.scale ? launch_norm<E, false, true>(p, s) : launch_norm<E, false, false>(p, s);
+}
+
+// ------------------------------------------------------------------------------------- gradients
+// A workgroup takes the rows blockIdx.x, blockIdx.x + strips, ... and keeps its part of dw in registers; the parts are
+// summed by a second launch in a fixed order.
+template <int E, int CH, int ENDS>
+__global__ __launch_bounds__(kMaxThreads) void norm_back_kernel(NormBackArgs p) {
+  __shared__ float red[2][kMaxThreads / 64];
+  const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * 8;
+  constexpr bool HELD = CH == 1;  // w too; in longer rows its registers are needed
+  float w[CH][8], dw[CH][8];
+#pragma unroll
+  for (int k = 0; k < CH; ++k) {
+    if (HELD) load_weight<E, ENDS>(p.w, p.w32, c0 + k * step, p.h, w[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
+  }
+  int odd = 0;
+  for (int64_t row = blockIdx.x; row < p.m; row += p.strips) {
+    const float rstd = p.rstd[row];
+    const char* dy = (const char*)p.dy + row * p.ld_dy * elt_size(E);
+    const char* xr = (const char*)p.x + row * p.ldx * elt_size(E);
+    float g[CH][8], x[CH][8], s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      load_cols<E, ENDS>(dy, c0 + k * step, p.h, g[k]);
+      load_cols<E, ENDS>(xr, c0 + k * step, p.h, x[k]);
+      if (!HELD) load_weight<E, ENDS>(p.w, p.w32, c0 + k * step, p.h, w[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[k][i] *= rstd;
+        dw[k][i] += g[k][i] * x[k][i];
+        g[k][i] *= w[k][i];
+        s += g[k][i] * x[k][i];
+      }
+    }
+    const float mean = block_sum(s, red[odd]) / (float)p.h;
+    odd ^= 1;
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      float d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) d[i] = rstd * (g[k][i] - x[k][i] * mean);
+      if (p.dres) {
+        float r[8];
+        load_cols<E, ENDS>((const char*)p.dres + row * p.ld_dres * elt_size(E), c0 + k * step, p.h, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] += r[i];
+      }
+      store_cols<E, ENDS>((char*)p.dx + row * p.ld_dx * elt_size(E), c0 + k * step, p.h, d);
+    }
+  }
+  char* part = (char*)(p.part + (int64_t)blockIdx.x * p.h);
+#pragma unroll
+  for (int k = 0; k < CH; ++k) store_cols<EL_F32, ENDS>(part, c0 + k * step, p.h, dw[k]);
+}
+
+// Rows too long for registers: dx row by row, then dw column by column.
+template <int E>
+__global__ __launch_bounds__(kMaxThreads) void norm_back_long_kernel(NormBackArgs p) {
+  __shared__ float red[kMaxThreads / 64];
+  const int64_t row = blockIdx.x;
+  const int step = (int)blockDim.x * 8;
+  const float rstd = p.rstd[row];
+  const char* dy = (const char*)p.dy + row * p.ld_dy * elt_size(E);
+  const char* xr = (const char*)p.x + row * p.ldx * elt_size(E);
+  float g[8], x[8], w[8], s = 0.0f;
+  for (int c = (int)threadIdx.x * 8; c < p.h; c += step) {
+    const int n = p.h - c;
+    load8<E>(dy + (int64_t)c * elt_size(E), n, g);
+    load8<E>(xr + (int64_t)c * elt_size(E), n, x);
+    load_weight<E, ANY>(p.w, p.w32, c, p.h, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += g[i] * w[i] * (x[i] * rstd);
+  }
+  const float mean = block_sum(s, red) / (float)p.h;
+  for (int c = (int)threadIdx.x * 8; c < p.h; c += step) {
+    const int n = p.h - c;
+    float d[8];
+    load8<E>(dy + (int64_t)c * elt_size(E), n, g);
+    load8<E>(xr + (int64_t)c * elt_size(E), n, x);
+    load_weight<E, ANY>(p.w, p.w32, c, p.h, w);
+    if (p.dres) load8<E>((const char*)p.dres + (row * p.ld_dres + c) * elt_size(E), n, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float v = rstd * (g[i] * w[i] - x[i] * rstd * mean);
+      d[i] = p.dres ? v + d[i] : v;
+    }
+    store8<E>((char*)p.dx + (row * p.ld_dx + c) * elt_size(E), n, d);
+  }
+}
+
+template <int E>
+__global__ __launch_bounds__(256) void norm_back_long_weight_kernel(NormBackArgs p) {
+  const int c = ((int)blockIdx.x * 256 + (int)threadIdx.x) * 8, n = p.h - c;
+  if (n <= 0) return;
+  float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int64_t row = blockIdx.y; row < p.m; row += p.strips) {
+    float g[8], x[8];
+    const float rstd = p.rstd[row];
+    load8<E>((const char*)p.dy + (row * p.ld_dy + c) * elt_size(E), n, g);
+    load8<E>((const char*)p.x + (row * p.ldx + c) * elt_size(E), n, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] += g[i] * (x[i] * rstd);
+  }
+  store8<EL_F32>((char*)(p.part + (int64_t)blockIdx.y * p.h + c), n, dw);
+}
+
+template <int E>
+hipError_t launch_back(const NormBackArgs& p, hipStream_t s) {
+  const int lanes = (p.h + 7) / 8;
+  const int threads = (lanes + 63) / 64 * 64;
+  if (p.h < 8) {
+    norm_back_kernel<E, 1, ANY><<<(unsigned)p.strips, threads, 0, s>>>(p);
+  } else if (lanes <= kMaxThreads) {
+    if (p.h % 8 == 0) norm_back_kernel<E, 1, WHOLE><<<(unsigned)p.strips, threads, 0, s>>>(p);
+    else norm_back_kernel<E, 1, CUT><<<(unsigned)p.strips, threads, 0, s>>>(p);
+  } else if (p.h % 8 == 0 && lanes <= 2 * kMaxThreads) {
+    norm_back_kernel<E, 2, WHOLE><<<(unsigned)p.strips, (threads / 2 + 63) / 64 * 64, 0, s>>>(p);
+  } else {
+    norm_back_long_kernel<E><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
+    norm_back_long_weight_kernel<E><<<dim3((unsigned)((lanes + 255) / 256), (unsigned)p.strips), 256, 0, s>>>(p);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_column_sums(p.part, p.strips, p.h, p.h, p.dw, s);
+}
+
+// ----------------------------------------------------------------------------------- column sums
+// 32 columns a workgroup, its 8 groups of lanes deal out the rows.
+constexpr int kSumCols = 32, kSumGroups = 256 / kSumCols;
+__global__ __launch_bounds__(256) void column_sums_kernel(const float* part, int rows, int64_t ld, int cols, float* out) {
+  __shared__ float red[kSumGroups][kSumCols];
+  const int l = (int)threadIdx.x % kSumCols, g = (int)threadIdx.x / kSumCols;
+  const int64_t c = (int64_t)blockIdx.x * kSumCols + l;
+  float s = 0.0f;
+  if (c < cols) {
+    for (int r = g; r < rows; r += kSumGroups) s += part[r * ld + c];
+  }
+  red[g][l] = s;
+  __syncthreads();
+  if (g == 0 && c < cols) {
+#pragma unroll
+    for (int i = 1; i < kSumGroups; ++i) s += red[i][l];
+    out[c] = s;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_column_sums(const float* part, int rows, int64_t ld, int cols, float* out, hipStream_t s) {
+  column_sums_kernel<<<(unsigned)((cols + kSumCols - 1) / kSumCols), 256, 0, s>>>(part, rows, ld, cols, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm(int elt, const NormArgs& p, hipStream_t s) {
+  if (elt == EL_F16) return launch_norm_e<EL_F16>(p, s);
+  if (elt == EL_BF16) return launch_norm_e<EL_BF16>(p, s);
+  return launch_norm_e<EL_F32>(p, s);
+}
+
+int norm_back_strips(int64_t m, int64_t h) {
+  constexpr int64_t kStrips = 512;
+  return (int)(m < kStrips ? m : kStrips);
+}
+
+hipError_t launch_rms_norm_backward(int elt, const NormBackArgs& p, hipStream_t s) {
+  if (elt == EL_F16) return launch_back<EL_F16>(p, s);
+  if (elt == EL_BF16) return launch_back<EL_BF16>(p, s);
+  return launch_back<EL_F32>(p, s);
+}
+
+}  // namespace ep

@@ -1,11 +1,13 @@
-"""Rows of a sparse (mixture-of-experts) layer: tokens sorted by expert, and back, with gradients.
+"""Rows of a sparse (mixture-of-experts) layer: tokens routed and sorted by expert, and back, with gradients.
 
+    ids, weights = expert_route(logits, topk)             # (T, k) each, of a router's logits (T, E)
     order = expert_order(ids, experts, align=128)         # ids (T, k): each token's experts
     rows = expert_dispatch(x, order)                      # (capacity, h), or quantize=True: (q, scale)
     ...                                                   # grouped products over order.offsets
     y = expert_combine(rows, order, weights)              # (T, h)
     drows, dweights = expert_combine_backward(dy, rows, order, weights)
     dx = expert_combine(drows, order)                     # the gradient of expert_dispatch
+    dlogits = expert_route_backward(dweights, logits, ids)
 
 Every function only enqueues kernels (libep.so, `ep_expert_*` in include/ep.h) on torch's current stream,
 or on `stream`, as under torch.cuda.stream(stream).  All are outside autograd: results carry no gradient, the gradients
@@ -21,7 +23,7 @@ from . import _check, lib
 from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
                          streamed, unit_columns)
 
-__all__ = ["ExpertOrder", "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
+__all__ = ["ExpertOrder", "expert_route", "expert_route_backward", "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
 
 
 class ExpertOrder(NamedTuple):
@@ -30,6 +32,64 @@ class ExpertOrder(NamedTuple):
     pos: torch.Tensor
     src: torch.Tensor
     offsets: torch.Tensor
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be softmax or sigmoid, got {score}")
+    return _SCORES[score]
+
+
+@streamed
+def expert_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups=None, group_top=2, renormalize=True, scale=1.0):
+    """(ids (T, topk) int32, weights (T, topk) float32) of a router's logits (T x E; float16, bfloat16 or float32): the topk experts
+    with the highest keys, in falling order, the lowest index first among equal ones.
+
+    An expert's key is its logit or, with a bias (E; float32) or groups, its score (softmax or sigmoid of the token's logits) plus
+    the bias, in double.  With groups > 1, groups of E / groups neighbouring experts, only the topk_groups (default: all) groups with
+    the greatest sum of their group_top (1 or 2) highest keys take part.  weights: scale times the chosen ones' scores (without bias), with
+    renormalize over their sum.  An expert with a logit or key of -infinity or NaN is never chosen; where fewer than topk can be,
+    the others' ids are -1 (which expert_order drops) with weight 0.  At most 1024 experts, 64 choices, 64 groups."""
+    check("logits", logits, ELT, (None, None))
+    t, e = logits.shape
+    kind = _score(score)
+    if not isinstance(topk, int) or topk < 1:
+        raise ValueError(f"topk must be a whole number of at least 1, got {topk}")
+    if bias is not None:
+        check("bias", bias, torch.float32, (e,), logits.device)
+        contiguous("bias", bias)
+    no_gradient("expert_route", logits, bias)
+    ld = unit_columns("logits", logits)
+    on_device(logits)
+    ids = torch.empty((t, topk), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((t, topk), dtype=torch.float32, device=logits.device)
+    _check(lib().ep_expert_route(logits.data_ptr(), t, e, ld, ELT[logits.dtype], None if bias is None else bias.data_ptr(), kind, groups,
+                                 groups if topk_groups is None else topk_groups, group_top, topk, int(bool(renormalize)), scale,
+                                 ids.data_ptr(), weights.data_ptr(), current_stream(logits)))
+    return ids, weights
+
+
+@streamed
+def expert_route_backward(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0):
+    """The gradient (T x E, the logits' type) of expert_route's logits for the gradient dweights (T, topk; float32) of its weights: ids
+    are its choice, which is constant (a bias has no gradient)."""
+    check("dweights", dweights, torch.float32, (None, None))
+    t, k = dweights.shape
+    check("logits", logits, ELT, (t, None), dweights.device)
+    check("ids", ids, torch.int32, (t, k), dweights.device)
+    contiguous("ids", ids)
+    kind = _score(score)
+    no_gradient("expert_route_backward", dweights, logits)
+    ld, ldw = unit_columns("logits", logits), unit_columns("dweights", dweights)
+    on_device(dweights)
+    e = logits.shape[1]
+    dlogits = torch.empty((t, e), dtype=logits.dtype, device=logits.device)
+    _check(lib().ep_expert_route_backward(dweights.data_ptr(), ldw, t, k, logits.data_ptr(), e, ld, ELT[logits.dtype], ids.data_ptr(),
+                                          kind, int(bool(renormalize)), scale, dlogits.data_ptr(), e, current_stream(logits)))
+    return dlogits
 
 
 @lru_cache(maxsize=256)

@@ -6,6 +6,8 @@ A matrix in this form is a pair (q, scale): q e4m3 values, scale one fp32 number
     xq, xs = quantize_fp8(x)                              # 1 x 128 blocks along the features
     wq, ws = quantize_fp8(w, block=(128, 128))
     y = matmul_fp8(xq, xs, wq, ws)                        # x w^T
+    h, p = matmul_fp8(xq, xs, wq, ws, bias=b, activation="gelu", save_pre=True)
+    d = epilogue_backward_fp8(dh, activation="gelu", pre=p)   # the operands of both gradients' products, the bias's gradient
 
 Every function only enqueues kernels (libep.so, `ep_*_fp8` in include/ep.h) on torch's current stream, or
 on `stream`, as under torch.cuda.stream(stream).  All are outside autograd: results carry no gradient, and a call
@@ -14,6 +16,7 @@ dy w by matmul_fp8 and grouped_matmul_fp8, dy^T x by grouped_wgrad_fp8 (one expe
 """
 import ctypes
 from functools import lru_cache
+from typing import NamedTuple
 
 import torch
 
@@ -21,7 +24,7 @@ from . import _check, lib
 from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
                          streamed, unit_columns)
 
-__all__ = ["quantize_fp8", "matmul_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8"]
+__all__ = ["quantize_fp8", "matmul_fp8", "EpilogueGradients", "epilogue_backward_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8"]
 
 
 @streamed
@@ -79,10 +82,27 @@ def _workspace(m, n, k):
     return need.value
 
 
+_ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _activation(activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None, relu, gelu or silu, got {activation}")
+    return _ACTIVATIONS[activation]
+
+
+def _same(a, b):
+    return a.data_ptr() == b.data_ptr() and a.stride() == b.stride()
+
+
 @streamed
-def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
+def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, bias=None, activation=None, residual=None, save_pre=False):
     """(a a_scale) (b b_scale)^T: a (M x K) with scales (M, ceil(K / 128)), b (N x K) with scales
     (ceil(N / 128), ceil(K / 128)); K a multiple of 16.  Summed in fp32, rounded once to out_dtype.
+
+    With an epilogue, p = a b^T + bias and the result is act(p) + residual, in fp32 before its one rounding: bias (N; out_dtype or
+    float32), activation "relu", "gelu" (exact) or "silu", residual (M x N; out_dtype).  `out` may be the residual itself.  save_pre
+    returns (result, p), p rounded to out_dtype, for epilogue_backward_fp8.
 
     16-bit outputs of more than 8 rows and K over 256 pass the e4m3 matrix instruction, which adds the products of 8
     neighbouring k in fixed point before fp32: each loses less than 2^-13 of the largest of the 8 (of normal
@@ -97,19 +117,94 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None):
     lda, ldb = _operand("a", a, (m, k)), _operand("b", b, (n, k))
     check("a_scale", a_scale, torch.float32, (m, blocks(k)), a.device)
     check("b_scale", b_scale, torch.float32, (blocks(n), blocks(k)), a.device)
-    no_gradient("matmul_fp8", a, a_scale, b, b_scale)
+    no_gradient("matmul_fp8", a, a_scale, b, b_scale, bias, residual)
+    epilog = bias is not None or activation is not None or residual is not None or save_pre
+    inputs = (a, a_scale, b, b_scale)
+    if epilog:
+        act = _activation(activation)
+        if bias is not None:
+            check("bias", bias, (out_dtype, torch.float32), (n,), a.device)
+            contiguous("bias", bias)
+            inputs += (bias,)
+        if residual is not None:
+            check("residual", residual, out_dtype, (m, n), a.device)
+            ld_res = unit_columns("residual", residual)
+            if out is None or not isinstance(out, torch.Tensor) or not _same(out, residual):
+                inputs += (residual,)
     on_device(a)
-    out, ldd = _out(out, out_dtype, (m, n), a, (a, a_scale, b, b_scale))
+    out, ldd = _out(out, out_dtype, (m, n), a, inputs)
+    pre = torch.empty((m, n), dtype=out_dtype, device=a.device) if save_pre else None
     if not m or not n:
-        return out
+        return (out, pre) if save_pre else out
     if not k:
+        if epilog:
+            raise ValueError("an epilogue needs a contracted length of at least 16")
         return out.zero_()
     need = _workspace(m, n, k)
     ws = torch.empty(need, dtype=torch.uint8, device=a.device) if need else None
-    _check(lib().ep_matmul_fp8(m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb,
-                           b_scale.data_ptr(), *b_scale.stride(), out.data_ptr(), ldd, ELT[out_dtype],
-                           ws.data_ptr() if need else None, need, current_stream(a)))
-    return out
+    product = (m, n, k, a.data_ptr(), lda, a_scale.data_ptr(), *a_scale.stride(), b.data_ptr(), ldb,
+               b_scale.data_ptr(), *b_scale.stride(), out.data_ptr(), ldd, ELT[out_dtype])
+    space = (ws.data_ptr() if need else None, need, current_stream(a))
+    if not epilog:
+        _check(lib().ep_matmul_fp8(*product, *space))
+        return out
+    _check(lib().ep_matmul_fp8_epilog(*product, None if bias is None else bias.data_ptr(), ELT[out_dtype if bias is None else bias.dtype],
+                                      act, None if residual is None else residual.data_ptr(), 0 if residual is None else ld_res,
+                                      pre.data_ptr() if save_pre else None, n, *space))
+    return (out, pre) if save_pre else out
+
+
+class EpilogueGradients(NamedTuple):
+    """q (M, N), scale (M, ceil(N / 128)): e4m3 rows of the gradient of p, an operand of the data gradient's product; q_t
+    (N, M), scale_t (N, ceil(M / 128)): of its transpose, an operand of the weight gradient's; dbias (N,) float32."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    q_t: torch.Tensor
+    scale_t: torch.Tensor
+    dbias: torch.Tensor
+
+
+@lru_cache(maxsize=256)
+def _backward_workspace(m, n):
+    """Bytes of the epilogue gradient's workspace, which depend on the sizes alone."""
+    need = ctypes.c_size_t()
+    _check(lib().ep_epilogue_backward_fp8_workspace(m, n, ctypes.byref(need)))
+    return need.value
+
+
+@streamed
+def epilogue_backward_fp8(dout, activation=None, pre=None):
+    """EpilogueGradients of matmul_fp8's epilogue for the gradient dout (M x N; float16, bfloat16 or float32) of its result: the
+    gradient of p is dout act'(pre), pre (M x N, dout's type) what save_pre gave (without an activation: None).  It is quantised
+    along both directions from its unrounded values (quantize_fp8's 1 x 128 blocks), and summed over the rows in fp32, in a
+    fixed order, to the bias's gradient.  The residual's gradient is dout itself.  M is any; as the contracted length of the weight
+    gradient's product it has to be a multiple of 16."""
+    check("dout", dout, ELT, (None, None))
+    m, n = dout.shape
+    act = _activation(activation)
+    if (pre is None) != (activation is None):
+        raise ValueError("pre is given with an activation, and only then")
+    if pre is not None:
+        check("pre", pre, dout.dtype, (m, n), dout.device)
+    no_gradient("epilogue_backward_fp8", dout, pre)
+    ld = unit_columns("dout", dout)
+    ldp = 0 if pre is None else unit_columns("pre", pre)
+    on_device(dout)
+    dev = dout.device
+    q = torch.empty((m, n), dtype=E4M3, device=dev)
+    q_t = torch.empty((n, m), dtype=E4M3, device=dev)
+    scale = torch.empty((blocks(n), m), dtype=torch.float32, device=dev)
+    scale_t = torch.empty((blocks(m), n), dtype=torch.float32, device=dev)
+    dbias = torch.empty((n,), dtype=torch.float32, device=dev)
+    if m and n:
+        need = _backward_workspace(m, n)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(lib().ep_epilogue_backward_fp8(dout.data_ptr(), m, n, ld, ELT[dout.dtype], act, None if pre is None else pre.data_ptr(), ldp,
+                                              q.data_ptr(), n, scale.data_ptr(), q_t.data_ptr(), m, scale_t.data_ptr(),
+                                              dbias.data_ptr(), ws.data_ptr(), need, current_stream(dout)))
+    else:
+        dbias.zero_()
+    return EpilogueGradients(q, scale.t(), q_t, scale_t.t(), dbias)
 
 
 def _offsets(offsets, experts, device):

@@ -1,0 +1,101 @@
+"""Root-mean-square norm of rows, with the residual's addition before it and 8-bit rows behind it, and its gradients.
+
+    n = rms_norm(x, weight, residual=stream, quantize=True)    # n.y, n.scale: an operand of matmul_fp8
+    ...                                                        # n.residual: the residual stream from here on
+    dx, dweight = rms_norm_backward(dy, n.residual, weight, n.rstd, dresidual=dstream)   # dx: of x and of the stream before
+
+Both only enqueue kernels (libep.so, `ep_rms_norm*` in include/ep.h) on torch's current stream, or on `stream`, as under
+torch.cuda.stream(stream), and are outside autograd: results carry no gradient, and a call that autograd would be
+expected to follow warns.
+"""
+import ctypes
+from functools import lru_cache
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import _check, lib
+from ._operators import (E4M3, ELT, blocks, check, contiguous, current_stream, no_gradient, on_device, streamed, unit_columns)
+
+__all__ = ["Normed", "rms_norm", "rms_norm_backward"]
+
+
+class Normed(NamedTuple):
+    """y (M, h): x's type or e4m3; scale (M, ceil(h / 128)) of e4m3 rows, else None; residual (M, h): what was
+    normalised (x itself without a residual); rstd (M,) float32."""
+    y: torch.Tensor
+    scale: Optional[torch.Tensor]
+    residual: torch.Tensor
+    rstd: torch.Tensor
+
+
+def _weight(weight, x):
+    check("weight", weight, (x.dtype, torch.float32), (x.shape[1],), x.device)
+    contiguous("weight", weight)
+
+
+@streamed
+def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False):
+    """Normed rows of x (M x h; float16, bfloat16 or float32): with r = x, or x + residual rounded to x's type, rstd =
+    (mean of r^2 + eps)^-1/2 and y = r rstd weight, in fp32, rounded once to x's type; or with quantize as quantize_fp8
+    makes e4m3 rows of the unrounded y (scale: features outermost in memory).  weight (h): x's type or float32."""
+    check("x", x, ELT, (None, None))
+    m, h = x.shape
+    _weight(weight, x)
+    if residual is not None:
+        check("residual", residual, x.dtype, (m, h), x.device)
+    if not 0 <= eps < float("inf"):
+        raise ValueError(f"eps must be finite and not negative, got {eps}")
+    no_gradient("rms_norm", x, weight, residual)
+    ldx = unit_columns("x", x)
+    ldr = 0 if residual is None else unit_columns("residual", residual)
+    on_device(x)
+    dev = x.device
+    total = x if residual is None else torch.empty((m, h), dtype=x.dtype, device=dev)
+    y = torch.empty((m, h), dtype=E4M3 if quantize else x.dtype, device=dev)
+    scale = torch.empty((blocks(h), m), dtype=torch.float32, device=dev) if quantize else None
+    rstd = torch.empty((m,), dtype=torch.float32, device=dev)
+    if m and h:
+        _check(lib().ep_rms_norm(x.data_ptr(), m, h, ldx, ELT[x.dtype], None if residual is None else residual.data_ptr(), ldr,
+                                 weight.data_ptr(), ELT[weight.dtype], eps, total.data_ptr(), h, y.data_ptr(), h,
+                                 scale.data_ptr() if quantize else None, rstd.data_ptr(), current_stream(x)))
+    elif m:
+        rstd.fill_(eps ** -0.5 if eps else float("inf"))
+    return Normed(y, scale.t() if quantize else None, total, rstd)
+
+
+@lru_cache(maxsize=256)
+def _workspace(m, h):
+    """Bytes of the gradients' workspace, which depend on the sizes alone."""
+    need = ctypes.c_size_t()
+    _check(lib().ep_rms_norm_backward_workspace(m, h, ctypes.byref(need)))
+    return need.value
+
+
+@streamed
+def rms_norm_backward(dy, x, weight, rstd, dresidual=None):
+    """(dx, dweight) of rms_norm for the gradient dy (M x h, x's type) of its output: x and rstd are its `residual` and
+    `rstd`.  dx (x's type) is the gradient of both x and the residual, with dresidual (M x h, x's type), the gradient that `residual`
+    has from elsewhere, added; dweight (h) is float32, summed in a fixed order."""
+    check("dy", dy, ELT, (None, None))
+    m, h = dy.shape
+    check("x", x, dy.dtype, (m, h), dy.device)
+    _weight(weight, x)
+    check("rstd", rstd, torch.float32, (m,), dy.device)
+    contiguous("rstd", rstd)
+    if dresidual is not None:
+        check("dresidual", dresidual, dy.dtype, (m, h), dy.device)
+    no_gradient("rms_norm_backward", dy, x, weight, rstd, dresidual)
+    ld_dy, ldx = unit_columns("dy", dy), unit_columns("x", x)
+    ldr = 0 if dresidual is None else unit_columns("dresidual", dresidual)
+    on_device(dy)
+    dx = torch.empty((m, h), dtype=dy.dtype, device=dy.device)
+    dweight = torch.empty((h,), dtype=torch.float32, device=dy.device)
+    if not m or not h:
+        return dx, dweight.zero_()
+    need = _workspace(m, h)
+    ws = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+    _check(lib().ep_rms_norm_backward(dy.data_ptr(), m, h, ld_dy, ELT[dy.dtype], x.data_ptr(), ldx, weight.data_ptr(),
+                                      ELT[weight.dtype], rstd.data_ptr(), None if dresidual is None else dresidual.data_ptr(), ldr,
+                                      dx.data_ptr(), h, dweight.data_ptr(), ws.data_ptr(), need, current_stream(dy)))
+    return dx, dweight

@@ -318,7 +318,28 @@ ep_status ep_matmul_fp8(int64_t m, int64_t n, int64_t k, const void* a, int64_t 
                         int64_t sa_k, const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d,
                         int64_t ldd, int out, void* workspace, size_t workspace_bytes, void* stream);
 
-/* ep_grouped_matmul_fp8: the same for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of a
+/* ep_matmul_fp8_epilog: the same with an epilogue: P = a b^T + bias, D = act(P) + residual, in fp32, D and (with pre non-null)
+ * P rounded once to `out`.  bias: n values of type bias_elt, EP_ELT_F32 or `out`, or NULL; residual and pre: m x n of type
+ * `out`, row strides ld_res (below 2^23) and ld_pre, or NULL.  The residual may be d itself (with its row stride).  Activations: EP_ACT_RELU
+ * (P > 0 ? P : 0), EP_ACT_GELU (P Phi(P), Phi the normal distribution function), EP_ACT_SILU (P / (1 + e^-P)).  The
+ * workspace is ep_matmul_fp8's. */
+typedef enum { EP_ACT_NONE = 0, EP_ACT_RELU = 1, EP_ACT_GELU = 2, EP_ACT_SILU = 3 } ep_activation;
+ep_status ep_matmul_fp8_epilog(int64_t m, int64_t n, int64_t k, const void* a, int64_t lda, const float* sa, int64_t sa_m,
+                               int64_t sa_k, const void* b, int64_t ldb, const float* sb, int64_t sb_n, int64_t sb_k, void* d,
+                               int64_t ldd, int out, const void* bias, int bias_elt, int activation, const void* residual,
+                               int64_t ld_res, void* pre, int64_t ld_pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ep_epilogue_backward_fp8: the gradient of that epilogue for dout (m x n, type elt), as the operands of the products that
+ * follow: with g = dout act'(pre) in fp32 (EP_ACT_NONE: g = dout, pre NULL; relu' is 1 where pre > 0), q (m x n) and scale
+ * as ep_quantize_fp8 makes them of g with 1 x 128 blocks, q_t (n x m) and scale_t the same of its transpose, and dbias[j] =
+ * sum over i of g[i][j] in fp32, in a fixed order.  The workspace (16-byte aligned) holds its partial sums.  At most 2^24 - 1
+ * blocks of 128 x 128. */
+ep_status ep_epilogue_backward_fp8_workspace(int64_t m, int64_t n, size_t* bytes);
+ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64_t ld, int elt, int activation, const void* pre,
+                                   int64_t ld_pre, void* q, int64_t ldq, float* scale, void* q_t, int64_t ldq_t, float* scale_t,
+                                   float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ep_grouped_matmul_fp8: ep_matmul_fp8 for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of a
  * (rows x k) times expert e's b (n x k at b + e * b_e, its scales at sb + e * sb_e).  offsets: experts + 1
  * whole numbers on the device, ascending from 0; rows from offsets[experts] on become zeros.  (An offset outside
  * 0 .. rows counts as the nearer end, one below an earlier one as that one; rows before offsets[0] are left alone.) */
@@ -360,6 +381,39 @@ ep_status ep_expert_combine(const void* y, int64_t rows, int64_t h, int64_t ldy,
 ep_status ep_expert_combine_backward(const void* dout, int64_t tokens, int64_t h, int64_t ld_dout, int elt, const void* y,
                                      int64_t rows, int64_t ldy, const int32_t* pos, int64_t topk, const int32_t* src,
                                      const float* w, int64_t ldw, void* dy, int64_t ld_dy, float* dw, void* stream);
+
+/* ep_expert_route: each token's experts and their weights.  logits: tokens x experts (at most 2^25 tokens, 1024 experts), bias:
+ * experts values or NULL.  score: EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID of the logits, one token at a time.  The key of an expert is its
+ * logit or, with a bias or more than one group, its score plus the bias, in double.  An expert whose logit or key is -infinity or NaN
+ * is never chosen.  groups (at most 64) of neighbouring experts: only experts of the topk_groups groups with the greatest sum of their group_top (1 or 2)
+ * highest keys are chosen from.  ids[t][j], weights[t][j] (topk, at most 64): the highest keys in falling order; among equal
+ * ones (of groups too) the lowest index comes first.  weights = scale * score, with renormalize scale * score / (sum of the chosen scores) (0 where
+ * that sum is 0).  Where fewer than topk experts can be chosen, the other ids are -1 with weight 0.
+ * ep_expert_route_backward: the gradient dlogits (tokens x experts, type elt) of the weights for theirs, dweights; the
+ * choice is constant.  ids below 0 or not below `experts` do not count, one given twice counts twice. */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score;
+ep_status ep_expert_route(const void* logits, int64_t tokens, int64_t experts, int64_t ld, int elt, const float* bias, int score,
+                          int64_t groups, int64_t topk_groups, int group_top, int64_t topk, int renormalize, double scale,
+                          int32_t* ids, float* weights, void* stream);
+ep_status ep_expert_route_backward(const float* dweights, int64_t ld_dw, int64_t tokens, int64_t topk, const void* logits,
+                                   int64_t experts, int64_t ld, int elt, const int32_t* ids, int score, int renormalize, double scale,
+                                   void* dlogits, int64_t ld_out, void* stream);
+
+/* ep_rms_norm: rows of x (m x h, h below 2^26) over their root mean square.  With a residual r = x + residual, rounded to x's
+ * type and stored in sum; without, r = x and sum is not used.  rstd[i] = (mean over j of r[i][j]^2 + eps)^(-1/2), y = r rstd
+ * weight in fp32, rounded once to x's type or, with scale non-null, quantised as ep_quantize_fp8 does with 1 x 128 blocks
+ * (y: e4m3, scale[c * m + i]).  weight: h values of weight_elt, EP_ELT_F32 or x's type.  sum may be x or the residual
+ * itself, with its row stride.
+ * ep_rms_norm_backward: dx[i][j] = rstd[i] (weight[j] dy[i][j] - r[i][j] rstd[i]^2 c[i]) + dresidual[i][j], c[i] = mean over j of
+ * weight dy r (x is r; dresidual may be NULL), the gradient of x and of the residual, and dweight[j] = sum over i of
+ * dy r rstd (fp32, in a fixed order; the workspace, 16-byte aligned, holds its parts). */
+ep_status ep_rms_norm(const void* x, int64_t m, int64_t h, int64_t ldx, int elt, const void* residual, int64_t ld_res,
+                      const void* weight, int weight_elt, double eps, void* sum, int64_t ld_sum, void* y, int64_t ldy, float* scale,
+                      float* rstd, void* stream);
+ep_status ep_rms_norm_backward_workspace(int64_t m, int64_t h, size_t* bytes);
+ep_status ep_rms_norm_backward(const void* dy, int64_t m, int64_t h, int64_t ld_dy, int elt, const void* x, int64_t ldx,
+                               const void* weight, int weight_elt, const float* rstd, const void* dresidual, int64_t ld_dres,
+                               void* dx, int64_t ld_dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Number of selectable tile configurations (valid ep_options.tile_cfg values). */
 int ep_num_tile_cfgs(void);
