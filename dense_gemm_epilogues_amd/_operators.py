@@ -81,6 +81,27 @@ def unit_columns(name, t):
     return ld
 
 
+def matrix(name, t, dtypes, shape, device=None):
+    """check and unit_columns of a matrix, in one look where it passes (a tuple of dtypes, or a dict of them)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes:
+        size, stride = t.shape, t.stride()
+        if len(size) == 2 and stride[1] == 1 and stride[0] >= size[1] and (device is None or t.device == device):
+            m, n = shape
+            if (m is None or m == size[0]) and (n is None or n == size[1]):
+                return stride[0]
+    check(name, t, dtypes, shape, device)
+    return unit_columns(name, t)
+
+
+def empty(shape, dtype, device, columns_outermost=False):
+    """An uninitialised tensor (torch.empty takes half as long again as this); a matrix with columns_outermost as the transpose of
+    a contiguous one."""
+    if len(shape) == 1:
+        return torch.empty_strided(shape, (1,), dtype=dtype, device=device)
+    m, n = shape
+    return torch.empty_strided(shape, (1, m or 1) if columns_outermost else (n or 1, 1), dtype=dtype, device=device)
+
+
 def contiguous(name, t):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, got stride {t.stride()}")

@@ -9,6 +9,12 @@ using namespace ep;
 
 namespace {
 
+// bytes of the parts of column sums; one part is the sum itself
+size_t parts_bytes(int64_t parts, int64_t cols) { return parts > 1 ? (size_t)parts * cols * 4 : 0; }
+bool workspace_fits(const void* workspace, size_t bytes, size_t need) {
+  return need == 0 || (workspace && bytes >= need && aligned(workspace, 16));
+}
+
 constexpr int64_t kMaxFeatures = (int64_t)1 << 26;
 constexpr int64_t kMaxThreads = (int64_t)1 << 32;  // of a launch, fewer than
 
@@ -64,7 +70,7 @@ ep_status ep_rms_norm_backward_workspace(int64_t m, int64_t h, size_t* bytes) {
   api_clear();
   EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
   *bytes = 0;
-  if (m >= 1 && h >= 1 && m < kMaxCount && h < kMaxFeatures) *bytes = (size_t)norm_back_strips(m, h) * h * 4;
+  if (m >= 1 && h >= 1 && m < kMaxCount && h < kMaxFeatures) *bytes = parts_bytes(norm_back_strips(m), h);
   return EP_OK;
 }
 
@@ -79,12 +85,12 @@ ep_status ep_rms_norm_backward(const void* dy, int64_t m, int64_t h, int64_t ld_
   EP_REQUIRE(aligned(dy, size) && aligned(x, size) && aligned(dresidual, size) && aligned(dx, size) && aligned(rstd, 4) &&
                  aligned(dweight, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
   EP_REQUIRE(ld_dy >= h && ldx >= h && ld_dx >= h && (!dresidual || ld_dres >= h), EP_ERR_INVALID_ARG, "row stride below the row length");
-  const int strips = norm_back_strips(m, h);
-  EP_REQUIRE(workspace && workspace_bytes >= (size_t)strips * h * 4 && aligned(workspace, 16), EP_ERR_INVALID_ARG,
+  const int strips = norm_back_strips(m);
+  EP_REQUIRE(workspace_fits(workspace, workspace_bytes, parts_bytes(strips, h)), EP_ERR_INVALID_ARG,
              "the workspace is not 16-byte aligned or smaller than ep_rms_norm_backward_workspace says");
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   NormBackArgs p{};
-  p.dy = dy; p.x = x; p.w = weight; p.rstd = rstd; p.dres = dresidual; p.dx = dx; p.dw = dweight; p.part = (float*)workspace;
+  p.dy = dy; p.x = x; p.w = weight; p.rstd = rstd; p.dres = dresidual; p.dx = dx; p.dw = dweight; p.part = strips > 1 ? (float*)workspace : dweight;
   p.ld_dy = ld_dy; p.ldx = ldx; p.ld_dres = ld_dres; p.ld_dx = ld_dx;
   p.m = (int)m; p.h = (int)h; p.w32 = weight_elt == EP_ELT_F32; p.strips = strips;
   return done(launch_rms_norm_backward(elt, p, (hipStream_t)stream), "rms_norm_backward");
@@ -137,7 +143,7 @@ ep_status ep_epilogue_backward_fp8_workspace(int64_t m, int64_t n, size_t* bytes
   api_clear();
   EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
   *bytes = 0;
-  if (m >= 1 && n >= 1 && m < kMaxCount && n < kMaxCount) *bytes = (size_t)((m + kScaleBlock - 1) / kScaleBlock) * n * 4;
+  if (m >= 1 && n >= 1 && m < kMaxCount && n < kMaxCount) *bytes = parts_bytes((m + kScaleBlock - 1) / kScaleBlock, n);
   return EP_OK;
 }
 
@@ -157,14 +163,14 @@ ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64
   EP_REQUIRE(ld >= n && (!pre || ld_pre >= n) && ldq >= n && ldq_t >= m, EP_ERR_INVALID_ARG, "row stride below the row length");
   const int64_t blocks = (m + kScaleBlock - 1) / kScaleBlock;
   EP_REQUIRE(blocks * ((n + kScaleBlock - 1) / kScaleBlock) < ((int64_t)1 << 24), EP_ERR_UNSUPPORTED, "the matrix has too many blocks for one launch");
-  EP_REQUIRE(workspace && workspace_bytes >= (size_t)blocks * n * 4 && aligned(workspace, 16), EP_ERR_INVALID_ARG,
+  EP_REQUIRE(workspace_fits(workspace, workspace_bytes, parts_bytes(blocks, n)), EP_ERR_INVALID_ARG,
              "the workspace is not 16-byte aligned or smaller than ep_epilogue_backward_fp8_workspace says");
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;
   EpilogBackArgs p{};
   p.dout = dout; p.pre = pre; p.ld = ld; p.ldp = ld_pre; p.m = (int)m; p.n = (int)n; p.act = activation;
-  p.q = (uint8_t*)q; p.scale = scale; p.qt = (uint8_t*)q_t; p.scale_t = scale_t; p.ldq = ldq; p.ldqt = ldq_t; p.part = (float*)workspace;
+  p.q = (uint8_t*)q; p.scale = scale; p.qt = (uint8_t*)q_t; p.scale_t = scale_t; p.ldq = ldq; p.ldqt = ldq_t; p.part = blocks > 1 ? (float*)workspace : dbias;
   const hipError_t e = launch_epilogue_backward(elt, p, (hipStream_t)stream);
-  if (e != hipSuccess) return done(e, "epilogue_backward_fp8");
+  if (e != hipSuccess || blocks == 1) return done(e, "epilogue_backward_fp8");
   return done(launch_column_sums(p.part, (int)blocks, n, (int)n, dbias, (hipStream_t)stream), "epilogue_backward_fp8");
 }
 

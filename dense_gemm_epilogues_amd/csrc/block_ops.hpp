@@ -30,13 +30,13 @@ struct NormBackArgs {
   const void* dres;                  // [m][h] added to dx, or null
   void* dx;                          // [m][h]
   float* dw;                         // [h]
-  float* part;                       // [strips][h]
+  float* part;                       // [strips][h]; of one strip dw itself
   int64_t ld_dy, ldx, ld_dres, ld_dx;
   int m, h;
   int w32;
   int strips;                        // workgroups the rows are dealt out to
 };
-int norm_back_strips(int64_t m, int64_t h);
+int norm_back_strips(int64_t m);
 hipError_t launch_rms_norm_backward(int elt, const NormBackArgs& p, hipStream_t s);
 
 // out[c] = sum over rows of part[row][c], rows ld apart, in a fixed order
@@ -54,6 +54,7 @@ struct RouteArgs {
   int64_t ld;
   int tokens, experts, topk;
   int score, groups, topk_groups, group_top, renormalize;
+  int shift;                         // 1 << shift lanes of a wave for each group, set by the launch
   double scale;
 };
 hipError_t launch_route(int elt, const RouteArgs& p, hipStream_t s);
@@ -80,7 +81,7 @@ struct EpilogBackArgs {
   uint8_t* qt;                       // [n][m] e4m3, scales [ceil(m / 128)][n]
   float* scale_t;
   int64_t ldq, ldqt;
-  float* part;                       // [ceil(m / 128)][n] column sums of row blocks
+  float* part;                       // [ceil(m / 128)][n] column sums of row blocks; of one block the result itself
 };
 hipError_t launch_epilogue_backward(int elt, const EpilogBackArgs& p, hipStream_t s);
 

@@ -6,130 +6,230 @@
 // One pass: a workgroup holds a 128 x 128 tile of g in registers, finds the maxima along both directions and its column
 // sums, and writes both quantisations, the transposed one through LDS.  Bound by HBM and, with an activation, nearly by
 // the arithmetic (46 instructions a value at the copy's rate).
+#include <type_traits>
+
 #include "block_ops.hpp"
 #include "fp8_epilog.hpp"
+#include "wave_ops.hpp"
 
 namespace ep {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kRows = kScaleBlock * 8 / kThreads, kStep = kScaleBlock / kRows;  // rows of a thread, so far apart
+constexpr uint32_t kInf = 0x7f800000u;
 
+// 16 values of a row as they are loaded: 8 registers of 16-bit values, 16 of fp32
 template <int E>
-__device__ __forceinline__ void load16(const char* p, int n, float* f) {
-  load8<E>(p, n, f);
-  load8<E>(p + 8 * elt_size(E), n - 8, f + 8);
+struct Raw {
+  u32x4 w[elt_size(E)];
+};
+template <int E>
+__device__ __forceinline__ Raw<E> load_raw(const char* p) {
+  Raw<E> r;
+#pragma unroll
+  for (int i = 0; i < elt_size(E); ++i) r.w[i] = *(const u32x4_u*)(p + 16 * i);
+  return r;
+}
+template <int E>
+__device__ __forceinline__ float value(const Raw<E>& r, int i) {
+  if constexpr (E == EL_F32) return elt_f32<E>(r.w[i / 4][i % 4]);
+  else return elt_f32<E>(i & 1 ? r.w[i / 8][i / 2 % 4] >> 16 : r.w[i / 8][i / 2 % 4] & 0xffffu);
 }
 
-__device__ __forceinline__ void put_bytes(uint8_t* q, int n, u32x4 w) {
-  if (n >= 16) {
-    *(u32x4_u*)q = w;
-  } else {
+struct MaxU {
+  __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
+struct Add {
+  __device__ float operator()(float a, float b) const { return a + b; }
+};
+
+// |v|'s bits, in the order of the values; infinities and NaN above all others, or with FINITE as 0
+template <bool FINITE>
+__device__ __forceinline__ uint32_t size_of(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v) & 0x7fffffffu;
+  if constexpr (!FINITE) return b;
+  int in = (int)(b - kInf) >> 31;  // (as bits: 64 truth values take more scalar registers than there are)
+  asm("" : "+v"(in));
+  return b & (uint32_t)in;
+}
+
+// f over the 8 lanes that hold the same 16 columns of 8 rows: lanes that differ in their bits 3 to 5.  Behind each of the last two
+// steps a lane keeps one of two columns, so that z[j] is column j + 4 (lane / 32) + 8 (lane / 16 % 2).
+template <class T, class F>
+__device__ __forceinline__ void over_rows(const T (&v)[16], T (&z)[4], F f) {
+  uint32_t x[16], y[8];
+  auto both = [&](uint32_t a, uint32_t b) __attribute__((always_inline)) {
+    return __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b)));
+  };
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < n) q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v[j]);
+    x[j] = both(b, (uint32_t)__builtin_amdgcn_mov_dpp((int)b, 0x128, 0xf, 0xf, true));  // row_ror:8
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const auto s = __builtin_amdgcn_permlane16_swap(x[j], x[j + 8], false, false);
+    y[j] = both(s[0], s[1]);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const auto s = __builtin_amdgcn_permlane32_swap(y[j], y[j + 4], false, false);
+    z[j] = __builtin_bit_cast(T, both(s[0], s[1]));
   }
 }
 
-// Thread t holds 16 columns, 16 (t % 8) .. + 15, of rows 32 i + t / 8.
-template <int E, int ACT>
-__global__ __launch_bounds__(kThreads) void epilogue_back_kernel(EpilogBackArgs p, int tiles_n) {
-  __shared__ float red[2][4][kScaleBlock];
-  __shared__ __align__(16) uint8_t tile[kScaleBlock * kScaleBlock];
-  const int tm = (int)(blockIdx.x / (unsigned)tiles_n), tn = (int)(blockIdx.x % (unsigned)tiles_n);
+struct Shared {
+  float amax[kWaves][kScaleBlock], sum[kWaves][kScaleBlock], inv[kScaleBlock];
+  uint8_t tile[kScaleBlock * kScaleBlock];
+};
+
+// 16-byte piece `sub` of row r of the e4m3 tile is kept as words 4 sub .. + 3 with their bits 2 to 4 changed by r / 8: the pieces
+// stay whole, and reads of one word of every eighth row spread over the banks
+__device__ __forceinline__ int word_of(int r, int word) { return r * (kScaleBlock / 4) + (word ^ ((r >> 3 & 7) << 2)); }
+
+// A 128 x 128 tile; thread t holds 16 columns, 16 (t % 8) .. + 15, of rows kStep i + t / 8.
+template <int E, int ACT, bool WHOLE>
+__device__ __forceinline__ void back_tile(const EpilogBackArgs& p, int tm, int tn, Shared& lds) {
   const int m0 = tm * kScaleBlock, n0 = tn * kScaleBlock;
   const int t = (int)threadIdx.x, sub = t & 7, rg = t >> 3, lane = lane_id(), wave = wave_id();
   const int col = n0 + sub * 16;
-  float f[4][16];
+  float f[kRows][16];
+  if constexpr (WHOLE) {
+    Raw<E> d[kRows], v[kRows];
+    const char* dp = (const char*)p.dout + ((int64_t)(m0 + rg) * p.ld + col) * elt_size(E);
+    const char* vp = (const char*)p.pre + ((int64_t)(m0 + rg) * p.ldp + col) * elt_size(E);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t row = m0 + 32 * i + rg;
-    const int n = row < p.m ? p.n - col : 0;
-    load16<E>((const char*)p.dout + (row * p.ld + col) * elt_size(E), n, f[i]);
-    if constexpr (ACT != ACT_NONE) {
-      float v[16];
-      load16<E>((const char*)p.pre + (row * p.ldp + col) * elt_size(E), n, v);
+    for (int i = 0; i < kRows; ++i) {
+      d[i] = load_raw<E>(dp + kStep * i * p.ld * elt_size(E));
+      if constexpr (ACT != ACT_NONE) v[i] = load_raw<E>(vp + kStep * i * p.ldp * elt_size(E));
+    }
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[i][j] = back_through<ACT>(f[i][j], v[j]);
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        f[i][j] = value<E>(d[i], j);
+        if constexpr (ACT != ACT_NONE) f[i][j] = back_through<ACT>(f[i][j], value<E>(v[i], j));
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t row = m0 + kStep * i + rg;
+      int n = row < p.m ? p.n - col : 0;
+      asm volatile("" : "+v"(n));  // (compared in each row: answers kept from one to the next take the scalar registers)
+#pragma unroll
+      for (int h = 0; h < 16; h += 8) load8<E>((const char*)p.dout + (row * p.ld + col + h) * elt_size(E), n - h, f[i] + h);
+      if constexpr (ACT != ACT_NONE) {
+#pragma unroll
+        for (int h = 0; h < 16; h += 8) {
+          float v[8];
+          load8<E>((const char*)p.pre + (row * p.ldp + col + h) * elt_size(E), n - h, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[i][h + j] = back_through<ACT>(f[i][h + j], v[j]);
+        }
+      }
     }
   }
-  // rows: 8 lanes a block
+  // the rows' maxima (8 lanes a block) and, over the wave's rows, the columns'
+  uint32_t row_max[kRows], col_max[16], z[4];
+  auto maxima = [&](auto finite) __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float amax = kAmaxMin;
+    for (int i = 0; i < kRows; ++i) {
+      uint32_t a = 0;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(f[i][j]));
-#pragma unroll
-    for (int d = 1; d < 8; d *= 2) amax = fmaxf(amax, __shfl_xor(amax, d));
-    const float inv = scale_inv(amax);
-    const int64_t row = m0 + 32 * i + rg;
-    if (row < p.m && col < p.n) {
-      u32x4 w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = to_e4m3x4(f[i][4 * j] * inv, f[i][4 * j + 1] * inv, f[i][4 * j + 2] * inv, f[i][4 * j + 3] * inv);
-      put_bytes(p.q + row * p.ldq + col, p.n - col, w);
-      if (sub == 0) p.scale[(int64_t)tn * p.m + row] = scale_of(amax);
+      for (int j = 0; j < 16; ++j) a = max(a, size_of<finite.value>(f[i][j]));
+      row_max[i] = lanes_reduce<8>(a, MaxU());
     }
-  }
-  // columns: maxima and sums over the thread's rows, the wave's and the four waves'
-  float amax[16], sum[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    amax[j] = kAmaxMin;
-    sum[j] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      amax[j] = fmaxf(amax[j], finite_abs(f[i][j]));
-      sum[j] += f[i][j];
-    }
-#pragma unroll
-    for (int d = 8; d < 64; d *= 2) {
-      amax[j] = fmaxf(amax[j], __shfl_xor(amax[j], d));
-      sum[j] += __shfl_xor(sum[j], d);
-    }
-  }
-  if (lane < 8) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      red[0][wave][lane * 16 + j] = amax[j];
-      red[1][wave][lane * 16 + j] = sum[j];
+      col_max[j] = size_of<finite.value>(f[0][j]);
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) col_max[j] = max(col_max[j], size_of<finite.value>(f[i][j]));
+    }
+  };
+  static_assert(kRows == 2, "rows");
+  maxima(std::false_type());
+  if (__ballot(max(row_max[0], row_max[1]) >= kInf)) maxima(std::true_type());
+  over_rows(col_max, z, MaxU());
+  const int at = sub * 16 + 8 * (lane >> 4 & 1) + 4 * (lane >> 5);
+  if (!(lane & 8)) *(u32x4*)&lds.amax[wave][at] = u32x4{z[0], z[1], z[2], z[3]};
+  {
+    float sum[16], s[4];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[j] = f[0][j] + f[1][j];
+    over_rows(sum, s, Add());
+    if (!(lane & 8)) *(f32x4*)&lds.sum[wave][at] = f32x4{s[0], s[1], s[2], s[3]};
+  }
+  // the rows' factors and scales: lane `sub` of a block divides for row sub % 2, the even pair 448 / amax, the odd one amax / 448
+  {
+    const float amax = fmaxf(__builtin_bit_cast(float, sub & 1 ? row_max[1] : row_max[0]), kAmaxMin);
+    const bool factor = !(sub & 2);
+    const float quot = (factor ? kF8Max : amax) / (factor ? amax : kF8Max);
+    const int64_t row = m0 + kStep * (sub & 1) + rg;
+    if (sub >> 1 == 1 && (WHOLE || row < p.m)) p.scale[(int64_t)tn * p.m + row] = quot;
+    // lanes 0 and 1 of each four hold the factors
+    const int q = __builtin_bit_cast(int, quot);
+    const float inv[2] = {__builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(q, 0x00, 0xf, 0xf, true)),
+                          __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(q, 0x55, 0xf, 0xf, true))};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t to = m0 + kStep * i + rg;
+      if (!WHOLE && (to >= p.m || col >= p.n)) continue;
+      u32x4 w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = to_e4m3x4(f[i][4 * j] * inv[i], f[i][4 * j + 1] * inv[i], f[i][4 * j + 2] * inv[i], f[i][4 * j + 3] * inv[i]);
+      uint8_t* q8 = p.q + to * p.ldq + col;
+      int n = p.n - col;
+      if (WHOLE || n >= 16) {
+        *(u32x4_u*)q8 = w;
+      } else {
+        asm volatile("" : "+v"(n));
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (e < n) q8[e] = (uint8_t)(w[e >> 2] >> (8 * (e & 3)));
+      }
     }
   }
   __syncthreads();
+  // the columns': thread t divides for column t % 128, the first 128 448 / amax, the second amax / 448, the third sum
+  {
+    const int c = t & (kScaleBlock - 1), part = t / kScaleBlock;
+    if (part < 2) {
+      float amax = kAmaxMin;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const int c = sub * 16 + j;
-    amax[j] = fmaxf(fmaxf(red[0][0][c], red[0][1][c]), fmaxf(red[0][2][c], red[0][3][c]));
+      for (int w = 0; w < kWaves; ++w) amax = fmaxf(amax, lds.amax[w][c]);
+      const float quot = (part == 0 ? kF8Max : amax) / (part == 0 ? amax : kF8Max);
+      if (part == 0) lds.inv[c] = quot;
+      else if (WHOLE || n0 + c < p.n) p.scale_t[(int64_t)tm * p.n + n0 + c] = quot;
+    } else if (part == 2 && (WHOLE || n0 + c < p.n)) {
+      float sum = lds.sum[0][c];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) sum += lds.sum[w][c];
+      p.part[(int64_t)tm * p.n + n0 + c] = sum;
+    }
   }
-  if (t < kScaleBlock && n0 + t < p.n)
-    p.part[(int64_t)tm * p.n + n0 + t] = (red[1][0][t] + red[1][1][t]) + (red[1][2][t] + red[1][3][t]);
-  if (rg == 0) {
+  __syncthreads();
+  f32x4 inv[4];
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      if (col + j < p.n) p.scale_t[(int64_t)tm * p.n + col + j] = scale_of(amax[j]);
-  }
+  for (int j = 0; j < 4; ++j) inv[j] = *(const f32x4*)&lds.inv[sub * 16 + 4 * j];
 #pragma unroll
-  for (int j = 0; j < 16; ++j) amax[j] = scale_inv(amax[j]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kRows; ++i) {
     u32x4 w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      w[j] = to_e4m3x4(f[i][4 * j] * amax[4 * j], f[i][4 * j + 1] * amax[4 * j + 1], f[i][4 * j + 2] * amax[4 * j + 2],
-                       f[i][4 * j + 3] * amax[4 * j + 3]);
-    }
-    // word kd of row r at kd ^ 8 (r / 16 % 4): the 16-byte pieces stay whole and the reads below spread over the banks
-    const int r = 32 * i + rg, pos = (sub * 4) ^ (((r >> 4) & 3) << 3);
-    *(u32x4*)(tile + r * kScaleBlock + pos * 4) = w;
+    for (int j = 0; j < 4; ++j)
+      w[j] = to_e4m3x4(f[i][4 * j] * inv[j][0], f[i][4 * j + 1] * inv[j][1], f[i][4 * j + 2] * inv[j][2], f[i][4 * j + 3] * inv[j][3]);
+    *(u32x4*)(lds.tile + word_of(kStep * i + rg, sub * 4) * 4) = w;
   }
   __syncthreads();
-  // 16 rows (of g) of 4 columns a thread: 16 words, transposed as 4 x 4 bytes
-  const int mg = t & 7, kd = t >> 3, pos = kd ^ ((mg & 3) << 3);
-  u32x4 out[4];
+  // 8 rows (of g) of 4 columns a thread: 8 words, transposed as 4 x 4 bytes
+  const int mg = t & 15, kd = t >> 4;
+  u32x2 out[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < 2; ++j) {
     uint32_t v[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = *(const uint32_t*)(tile + (mg * 16 + 4 * j + e) * kScaleBlock + pos * 4);
+    for (int e = 0; e < 4; ++e) v[e] = *(const uint32_t*)(lds.tile + word_of(mg * 8 + 4 * j + e, kd) * 4);
     const uint32_t lo01 = __builtin_amdgcn_perm(v[1], v[0], 0x05010400u);  // v0.0 v1.0 v0.1 v1.1
     const uint32_t hi01 = __builtin_amdgcn_perm(v[1], v[0], 0x07030602u);  // v0.2 v1.2 v0.3 v1.3
     const uint32_t lo23 = __builtin_amdgcn_perm(v[3], v[2], 0x05010400u);
@@ -139,14 +239,29 @@ __global__ __launch_bounds__(kThreads) void epilogue_back_kernel(EpilogBackArgs 
     out[2][j] = __builtin_amdgcn_perm(hi23, hi01, 0x05040100u);
     out[3][j] = __builtin_amdgcn_perm(hi23, hi01, 0x07060302u);
   }
-  const int mm = m0 + mg * 16;
-  if (mm < p.m) {
+  const int mm = m0 + mg * 8;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int n = n0 + 4 * kd + b;
-      if (n < p.n) put_bytes(p.qt + (int64_t)n * p.ldqt + mm, p.m - mm, out[b]);
+  for (int b = 0; b < 4; ++b) {
+    const int n = n0 + 4 * kd + b;
+    uint8_t* q8 = p.qt + (int64_t)n * p.ldqt + mm;
+    int left = WHOLE ? 8 : n < p.n ? p.m - mm : 0;
+    if (WHOLE || left >= 8) {
+      *(u32x2_u*)q8 = out[b];
+    } else {
+      asm volatile("" : "+v"(left));
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (e < left) q8[e] = (uint8_t)(out[b][e >> 2] >> (8 * (e & 3)));
     }
   }
+}
+
+template <int E, int ACT>
+__global__ __launch_bounds__(kThreads) void epilogue_back_kernel(EpilogBackArgs p, int tiles_n) {
+  __shared__ __align__(16) Shared lds;
+  const int tm = (int)(blockIdx.x / (unsigned)tiles_n), tn = (int)(blockIdx.x % (unsigned)tiles_n);
+  if ((tm + 1) * kScaleBlock <= p.m && (tn + 1) * kScaleBlock <= p.n) back_tile<E, ACT, true>(p, tm, tn, lds);
+  else back_tile<E, ACT, false>(p, tm, tn, lds);
 }
 
 template <int E>

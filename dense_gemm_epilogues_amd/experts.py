@@ -20,8 +20,8 @@ from typing import NamedTuple
 import torch
 
 from . import _check, lib
-from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
-                         streamed, unit_columns)
+from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, empty, matrix, no_gradient,
+                         on_device, streamed, unit_columns)
 
 __all__ = ["ExpertOrder", "expert_route", "expert_route_backward", "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
 
@@ -53,7 +53,7 @@ def expert_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups
     the greatest sum of their group_top (1 or 2) highest keys take part.  weights: scale times the chosen ones' scores (without bias), with
     renormalize over their sum.  An expert with a logit or key of -infinity or NaN is never chosen; where fewer than topk can be,
     the others' ids are -1 (which expert_order drops) with weight 0.  At most 1024 experts, 64 choices, 64 groups."""
-    check("logits", logits, ELT, (None, None))
+    ld = matrix("logits", logits, ELT, (None, None))
     t, e = logits.shape
     kind = _score(score)
     if not isinstance(topk, int) or topk < 1:
@@ -62,10 +62,9 @@ def expert_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups
         check("bias", bias, torch.float32, (e,), logits.device)
         contiguous("bias", bias)
     no_gradient("expert_route", logits, bias)
-    ld = unit_columns("logits", logits)
     on_device(logits)
-    ids = torch.empty((t, topk), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((t, topk), dtype=torch.float32, device=logits.device)
+    dev = logits.device
+    ids, weights = empty((t, topk), torch.int32, dev), empty((t, topk), torch.float32, dev)
     _check(lib().ep_expert_route(logits.data_ptr(), t, e, ld, ELT[logits.dtype], None if bias is None else bias.data_ptr(), kind, groups,
                                  groups if topk_groups is None else topk_groups, group_top, topk, int(bool(renormalize)), scale,
                                  ids.data_ptr(), weights.data_ptr(), current_stream(logits)))
@@ -76,17 +75,17 @@ def expert_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups
 def expert_route_backward(dweights, logits, ids, score="softmax", renormalize=True, scale=1.0):
     """The gradient (T x E, the logits' type) of expert_route's logits for the gradient dweights (T, topk; float32) of its weights: ids
     are its choice, which is constant (a bias has no gradient)."""
-    check("dweights", dweights, torch.float32, (None, None))
+    ldw = matrix("dweights", dweights, (torch.float32,), (None, None))
     t, k = dweights.shape
-    check("logits", logits, ELT, (t, None), dweights.device)
-    check("ids", ids, torch.int32, (t, k), dweights.device)
+    dev = dweights.device
+    ld = matrix("logits", logits, ELT, (t, None), dev)
+    check("ids", ids, torch.int32, (t, k), dev)
     contiguous("ids", ids)
     kind = _score(score)
     no_gradient("expert_route_backward", dweights, logits)
-    ld, ldw = unit_columns("logits", logits), unit_columns("dweights", dweights)
     on_device(dweights)
     e = logits.shape[1]
-    dlogits = torch.empty((t, e), dtype=logits.dtype, device=logits.device)
+    dlogits = empty((t, e), logits.dtype, dev)
     _check(lib().ep_expert_route_backward(dweights.data_ptr(), ldw, t, k, logits.data_ptr(), e, ld, ELT[logits.dtype], ids.data_ptr(),
                                           kind, int(bool(renormalize)), scale, dlogits.data_ptr(), e, current_stream(logits)))
     return dlogits

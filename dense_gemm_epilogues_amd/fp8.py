@@ -21,8 +21,8 @@ from typing import NamedTuple
 import torch
 
 from . import _check, lib
-from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, no_gradient, on_device,
-                         streamed, unit_columns)
+from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, empty, matrix, no_gradient,
+                         on_device, streamed, unit_columns)
 
 __all__ = ["quantize_fp8", "matmul_fp8", "EpilogueGradients", "epilogue_backward_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8"]
 
@@ -127,13 +127,12 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, bias=
             contiguous("bias", bias)
             inputs += (bias,)
         if residual is not None:
-            check("residual", residual, out_dtype, (m, n), a.device)
-            ld_res = unit_columns("residual", residual)
+            ld_res = matrix("residual", residual, (out_dtype,), (m, n), a.device)
             if out is None or not isinstance(out, torch.Tensor) or not _same(out, residual):
                 inputs += (residual,)
     on_device(a)
     out, ldd = _out(out, out_dtype, (m, n), a, inputs)
-    pre = torch.empty((m, n), dtype=out_dtype, device=a.device) if save_pre else None
+    pre = empty((m, n), out_dtype, a.device) if save_pre else None
     if not m or not n:
         return (out, pre) if save_pre else out
     if not k:
@@ -179,32 +178,28 @@ def epilogue_backward_fp8(dout, activation=None, pre=None):
     along both directions from its unrounded values (quantize_fp8's 1 x 128 blocks), and summed over the rows in fp32, in a
     fixed order, to the bias's gradient.  The residual's gradient is dout itself.  M is any; as the contracted length of the weight
     gradient's product it has to be a multiple of 16."""
-    check("dout", dout, ELT, (None, None))
+    ld = matrix("dout", dout, ELT, (None, None))
     m, n = dout.shape
+    dev = dout.device
     act = _activation(activation)
     if (pre is None) != (activation is None):
         raise ValueError("pre is given with an activation, and only then")
-    if pre is not None:
-        check("pre", pre, dout.dtype, (m, n), dout.device)
+    ldp = 0 if pre is None else matrix("pre", pre, (dout.dtype,), (m, n), dev)
     no_gradient("epilogue_backward_fp8", dout, pre)
-    ld = unit_columns("dout", dout)
-    ldp = 0 if pre is None else unit_columns("pre", pre)
     on_device(dout)
-    dev = dout.device
-    q = torch.empty((m, n), dtype=E4M3, device=dev)
-    q_t = torch.empty((n, m), dtype=E4M3, device=dev)
-    scale = torch.empty((blocks(n), m), dtype=torch.float32, device=dev)
-    scale_t = torch.empty((blocks(m), n), dtype=torch.float32, device=dev)
-    dbias = torch.empty((n,), dtype=torch.float32, device=dev)
+    q, q_t = empty((m, n), E4M3, dev), empty((n, m), E4M3, dev)
+    scale = empty((m, blocks(n)), torch.float32, dev, columns_outermost=True)
+    scale_t = empty((n, blocks(m)), torch.float32, dev, columns_outermost=True)
+    dbias = empty((n,), torch.float32, dev)
     if m and n:
         need = _backward_workspace(m, n)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = empty((need,), torch.uint8, dev) if need else None
         _check(lib().ep_epilogue_backward_fp8(dout.data_ptr(), m, n, ld, ELT[dout.dtype], act, None if pre is None else pre.data_ptr(), ldp,
                                               q.data_ptr(), n, scale.data_ptr(), q_t.data_ptr(), m, scale_t.data_ptr(),
-                                              dbias.data_ptr(), ws.data_ptr(), need, current_stream(dout)))
+                                              dbias.data_ptr(), ws.data_ptr() if need else None, need, current_stream(dout)))
     else:
         dbias.zero_()
-    return EpilogueGradients(q, scale.t(), q_t, scale_t.t(), dbias)
+    return EpilogueGradients(q, scale, q_t, scale_t, dbias)
 
 
 def _offsets(offsets, experts, device):

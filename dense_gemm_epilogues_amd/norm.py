@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _check, lib
-from ._operators import (E4M3, ELT, blocks, check, contiguous, current_stream, no_gradient, on_device, streamed, unit_columns)
+from ._operators import E4M3, ELT, blocks, check, contiguous, current_stream, empty, matrix, no_gradient, on_device, streamed
 
 __all__ = ["Normed", "rms_norm", "rms_norm_backward"]
 
@@ -39,29 +39,26 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False):
     """Normed rows of x (M x h; float16, bfloat16 or float32): with r = x, or x + residual rounded to x's type, rstd =
     (mean of r^2 + eps)^-1/2 and y = r rstd weight, in fp32, rounded once to x's type; or with quantize as quantize_fp8
     makes e4m3 rows of the unrounded y (scale: features outermost in memory).  weight (h): x's type or float32."""
-    check("x", x, ELT, (None, None))
+    ldx = matrix("x", x, ELT, (None, None))
     m, h = x.shape
+    dev = x.device
     _weight(weight, x)
-    if residual is not None:
-        check("residual", residual, x.dtype, (m, h), x.device)
+    ldr = 0 if residual is None else matrix("residual", residual, (x.dtype,), (m, h), dev)
     if not 0 <= eps < float("inf"):
         raise ValueError(f"eps must be finite and not negative, got {eps}")
     no_gradient("rms_norm", x, weight, residual)
-    ldx = unit_columns("x", x)
-    ldr = 0 if residual is None else unit_columns("residual", residual)
     on_device(x)
-    dev = x.device
-    total = x if residual is None else torch.empty((m, h), dtype=x.dtype, device=dev)
-    y = torch.empty((m, h), dtype=E4M3 if quantize else x.dtype, device=dev)
-    scale = torch.empty((blocks(h), m), dtype=torch.float32, device=dev) if quantize else None
-    rstd = torch.empty((m,), dtype=torch.float32, device=dev)
+    total = x if residual is None else empty((m, h), x.dtype, dev)
+    y = empty((m, h), E4M3 if quantize else x.dtype, dev)
+    scale = empty((m, blocks(h)), torch.float32, dev, columns_outermost=True) if quantize else None
+    rstd = empty((m,), torch.float32, dev)
     if m and h:
         _check(lib().ep_rms_norm(x.data_ptr(), m, h, ldx, ELT[x.dtype], None if residual is None else residual.data_ptr(), ldr,
                                  weight.data_ptr(), ELT[weight.dtype], eps, total.data_ptr(), h, y.data_ptr(), h,
                                  scale.data_ptr() if quantize else None, rstd.data_ptr(), current_stream(x)))
     elif m:
         rstd.fill_(eps ** -0.5 if eps else float("inf"))
-    return Normed(y, scale.t() if quantize else None, total, rstd)
+    return Normed(y, scale, total, rstd)
 
 
 @lru_cache(maxsize=256)
@@ -77,25 +74,23 @@ def rms_norm_backward(dy, x, weight, rstd, dresidual=None):
     """(dx, dweight) of rms_norm for the gradient dy (M x h, x's type) of its output: x and rstd are its `residual` and
     `rstd`.  dx (x's type) is the gradient of both x and the residual, with dresidual (M x h, x's type), the gradient that `residual`
     has from elsewhere, added; dweight (h) is float32, summed in a fixed order."""
-    check("dy", dy, ELT, (None, None))
+    ld_dy = matrix("dy", dy, ELT, (None, None))
     m, h = dy.shape
-    check("x", x, dy.dtype, (m, h), dy.device)
+    dev, same = dy.device, (dy.dtype,)
+    ldx = matrix("x", x, same, (m, h), dev)
     _weight(weight, x)
-    check("rstd", rstd, torch.float32, (m,), dy.device)
+    check("rstd", rstd, torch.float32, (m,), dev)
     contiguous("rstd", rstd)
-    if dresidual is not None:
-        check("dresidual", dresidual, dy.dtype, (m, h), dy.device)
+    ldr = 0 if dresidual is None else matrix("dresidual", dresidual, same, (m, h), dev)
     no_gradient("rms_norm_backward", dy, x, weight, rstd, dresidual)
-    ld_dy, ldx = unit_columns("dy", dy), unit_columns("x", x)
-    ldr = 0 if dresidual is None else unit_columns("dresidual", dresidual)
     on_device(dy)
-    dx = torch.empty((m, h), dtype=dy.dtype, device=dy.device)
-    dweight = torch.empty((h,), dtype=torch.float32, device=dy.device)
+    dx = empty((m, h), dy.dtype, dev)
+    dweight = empty((h,), torch.float32, dev)
     if not m or not h:
         return dx, dweight.zero_()
     need = _workspace(m, h)
-    ws = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+    ws = empty((need,), torch.uint8, dev) if need else None
     _check(lib().ep_rms_norm_backward(dy.data_ptr(), m, h, ld_dy, ELT[dy.dtype], x.data_ptr(), ldx, weight.data_ptr(),
                                       ELT[weight.dtype], rstd.data_ptr(), None if dresidual is None else dresidual.data_ptr(), ldr,
-                                      dx.data_ptr(), h, dweight.data_ptr(), ws.data_ptr(), need, current_stream(dy)))
+                                      dx.data_ptr(), h, dweight.data_ptr(), ws.data_ptr() if need else None, need, current_stream(dy)))
     return dx, dweight

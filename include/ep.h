@@ -332,8 +332,9 @@ ep_status ep_matmul_fp8_epilog(int64_t m, int64_t n, int64_t k, const void* a, i
 /* ep_epilogue_backward_fp8: the gradient of that epilogue for dout (m x n, type elt), as the operands of the products that
  * follow: with g = dout act'(pre) in fp32 (EP_ACT_NONE: g = dout, pre NULL; relu' is 1 where pre > 0), q (m x n) and scale
  * as ep_quantize_fp8 makes them of g with 1 x 128 blocks, q_t (n x m) and scale_t the same of its transpose, and dbias[j] =
- * sum over i of g[i][j] in fp32, in a fixed order.  The workspace (16-byte aligned) holds its partial sums.  At most 2^24 - 1
- * blocks of 128 x 128. */
+ * sum over i of g[i][j] in fp32, in a fixed order.  The workspace (16-byte aligned, of ep_epilogue_backward_fp8_workspace bytes, none for up to
+ * 128 rows) holds its partial sums.  At most 2^24 - 1
+ * * blocks of 128 x 128. */
 ep_status ep_epilogue_backward_fp8_workspace(int64_t m, int64_t n, size_t* bytes);
 ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64_t ld, int elt, int activation, const void* pre,
                                    int64_t ld_pre, void* q, int64_t ldq, float* scale, void* q_t, int64_t ldq_t, float* scale_t,
@@ -406,7 +407,8 @@ ep_status ep_expert_route_backward(const float* dweights, int64_t ld_dw, int64_t
  * itself, with its row stride.
  * ep_rms_norm_backward: dx[i][j] = rstd[i] (weight[j] dy[i][j] - r[i][j] rstd[i]^2 c[i]) + dresidual[i][j], c[i] = mean over j of
  * weight dy r (x is r; dresidual may be NULL), the gradient of x and of the residual, and dweight[j] = sum over i of
- * dy r rstd (fp32, in a fixed order; the workspace, 16-byte aligned, holds its parts). */
+ * dy r rstd (fp32, in a fixed order; the workspace, 16-byte aligned, of
+ * ep_rms_norm_backward_workspace bytes, possibly none, holds its parts). */
 ep_status ep_rms_norm(const void* x, int64_t m, int64_t h, int64_t ldx, int elt, const void* residual, int64_t ld_res,
                       const void* weight, int weight_elt, double eps, void* sum, int64_t ld_sum, void* y, int64_t ldy, float* scale,
                       float* rstd, void* stream);

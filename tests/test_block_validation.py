@@ -170,6 +170,7 @@ def test_norm_abi():
     need = ctypes.c_size_t(7)
     L = ep.lib()
     assert L.ep_rms_norm_backward_workspace(9000, 5003, ctypes.byref(need)) == 0 and need.value % (5003 * 4) == 0 and need.value >= 5003 * 4
+    assert L.ep_rms_norm_backward_workspace(1, 5003, ctypes.byref(need)) == 0 and need.value == 0
     assert L.ep_rms_norm_backward_workspace(1, 1, None) == INVALID
     assert L.ep_rms_norm_backward_workspace(4, 8, ctypes.byref(need)) == 0
     size = need.value
@@ -203,9 +204,10 @@ def test_epilogue_abi():
                                                                                           "ldr": 512, "ldp": 512, "sak": 128}, INVALID)))
     need = ctypes.c_size_t(7)
     assert ep.lib().ep_epilogue_backward_fp8_workspace(300, 70, ctypes.byref(need)) == 0 and need.value == 3 * 70 * 4
+    assert ep.lib().ep_epilogue_backward_fp8_workspace(128, 70, ctypes.byref(need)) == 0 and need.value == 0
     assert ep.lib().ep_epilogue_backward_fp8_workspace(300, 70, None) == INVALID
-    refused(abi("ep_epilogue_backward_fp8", dict(g=P, m=4, n=8, ld=8, elt=1, act=1, pre=P, ldp=8, q=P, ldq=8, s=P, qt=P, ldqt=4, st_=P, db=P, ws=P, wsb=32, st=None)), (
+    refused(abi("ep_epilogue_backward_fp8", dict(g=P, m=200, n=8, ld=8, elt=1, act=1, pre=P, ldp=8, q=P, ldq=8, s=P, qt=P, ldqt=200, st_=P, db=P, ws=P, wsb=64, st=None)), (
         ({"m": 0}, INVALID), ({"n": 2 ** 31}, UNSUPPORTED), ({"elt": 3}, UNSUPPORTED), ({"act": 4}, UNSUPPORTED), ({"pre": None}, INVALID), ({"act": 0}, INVALID),
         ({"g": None}, INVALID), ({"q": None}, INVALID), ({"s": None}, INVALID), ({"qt": None}, INVALID), ({"st_": None}, INVALID), ({"db": None}, INVALID),
-        ({"ld": 7}, INVALID), ({"ldp": 7}, INVALID), ({"ldq": 7}, INVALID), ({"ldqt": 3}, INVALID), ({"ws": None}, INVALID), ({"wsb": 31}, INVALID),
+        ({"ld": 7}, INVALID), ({"ldp": 7}, INVALID), ({"ldq": 7}, INVALID), ({"ldqt": 199}, INVALID), ({"ws": None}, INVALID), ({"wsb": 63}, INVALID),
         ({"ws": P + 8}, INVALID), ({"pre": P + 1}, INVALID), ({"m": 2 ** 20, "n": 2 ** 20, "ld": 2 ** 20, "ldp": 2 ** 20, "ldq": 2 ** 20, "ldqt": 2 ** 20}, UNSUPPORTED)))
