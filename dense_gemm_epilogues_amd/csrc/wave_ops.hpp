@@ -5,12 +5,11 @@
 
 namespace ep {
 
-// lane ^ D of an already reduced group of D lanes: within 16 lanes the mirrored half or row holds the same value
+// lane ^ D of an already reduced group of D lanes, D up to 8: the mirrored half or row holds the same value
 template <int D>
 __device__ __forceinline__ uint32_t lane_xor32(uint32_t v) {
   constexpr int ctrl = D == 1 ? 0xb1 : D == 2 ? 0x4e : D == 4 ? 0x141 : 0x140;  // quad_perm [1,0,3,2], [2,3,0,1], row_half_mirror, row_mirror
-  if constexpr (D < 16) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xf, 0xf, true);
-  else return (uint32_t)__shfl_xor((int)v, D);
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, ctrl, 0xf, 0xf, true);
 }
 template <int D, class T>
 __device__ __forceinline__ T lane_xor(T v) {
@@ -22,6 +21,37 @@ __device__ __forceinline__ T lane_xor(T v) {
   }
 }
 
+// f of what lanes D apart hold, D 16 or 32, in all of them
+template <int D, class F>
+__device__ __forceinline__ uint32_t across32(uint32_t v, F f) {
+  if constexpr (D == 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return f((uint32_t)s[0], (uint32_t)s[1]);
+  } else {
+    const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return f((uint32_t)s[0], (uint32_t)s[1]);
+  }
+}
+template <int D, class T, class F>
+__device__ __forceinline__ T across(T v, F f) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, across32<D>(__builtin_bit_cast(uint32_t, v), [&](uint32_t a, uint32_t b) {
+      return __builtin_bit_cast(uint32_t, f(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b)));
+    }));
+  } else {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    uint32_t lo[2], hi[2];
+    if constexpr (D == 16) {
+      const auto l = __builtin_amdgcn_permlane16_swap((uint32_t)b, (uint32_t)b, false, false), h = __builtin_amdgcn_permlane16_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+      lo[0] = l[0], lo[1] = l[1], hi[0] = h[0], hi[1] = h[1];
+    } else {
+      const auto l = __builtin_amdgcn_permlane32_swap((uint32_t)b, (uint32_t)b, false, false), h = __builtin_amdgcn_permlane32_swap((uint32_t)(b >> 32), (uint32_t)(b >> 32), false, false);
+      lo[0] = l[0], lo[1] = l[1], hi[0] = h[0], hi[1] = h[1];
+    }
+    return f(__builtin_bit_cast(T, (uint64_t)hi[0] << 32 | lo[0]), __builtin_bit_cast(T, (uint64_t)hi[1] << 32 | lo[1]));
+  }
+}
+
 // f over L neighbouring lanes, in every one of them; f is associative and commutative (the sums' order is fixed: the same in all lanes)
 template <int L, class T, class F>
 __device__ __forceinline__ T lanes_reduce(T v, F f) {
@@ -29,8 +59,8 @@ __device__ __forceinline__ T lanes_reduce(T v, F f) {
   if constexpr (L > 2) v = f(v, lane_xor<2>(v));
   if constexpr (L > 4) v = f(v, lane_xor<4>(v));
   if constexpr (L > 8) v = f(v, lane_xor<8>(v));
-  if constexpr (L > 16) v = f(v, lane_xor<16>(v));
-  if constexpr (L > 32) v = f(v, lane_xor<32>(v));
+  if constexpr (L > 16) v = across<16>(v, f);
+  if constexpr (L > 32) v = across<32>(v, f);
   return v;
 }
 

@@ -91,6 +91,30 @@ def test_far_logits():
         assert ((w.cpu() - ww).abs() <= 2.0 ** -15 * ww + 2.0 ** -140).all()  # (e^200: the argument's rounding, 200 2^-24)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("e,topk,kw", [
+    (8, 2, {}), (60, 6, {"score": "sigmoid"}), (64, 16, {"bias": 1}), (64, 17, {}), (128, 4, {"score": "sigmoid", "groups": 8, "topk_groups": 3}),
+    (160, 6, {"groups": 8, "topk_groups": 4, "group_top": 1}), (256, 8, {"score": "sigmoid", "bias": 1, "groups": 8, "topk_groups": 4}), (256, 33, {"bias": 1}),
+    (200, 20, {"score": "sigmoid", "renormalize": False}), (384, 8, {"groups": 8, "topk_groups": 4})])
+def test_many_tokens(dtype, e, topk, kw):
+    """As many as share a wave, the last one not full; among them tokens of equal, masked and infinite logits."""
+    t = 4099
+    g = B.gen(e + topk)
+    logits = (2 * torch.randn((t, e), generator=g)).clamp(-8, 8)
+    logits[::7] = logits[::7].round()
+    logits[5::50, e // 3:] = -math.inf
+    logits[6::90] = math.nan
+    logits[7::90, 3] = math.inf
+    logits = logits.to(dtype)
+    kw = dict(kw)
+    if "bias" in kw:
+        kw["bias"] = 0.1 * torch.randn(e, generator=g)
+    ids, w = check_route(logits, topk, **kw)
+    dev = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+    few = [ep.expert_route(logits[i:i + 1000].cuda(), topk, **dev) for i in range(0, t, 1000)]
+    assert torch.equal(torch.cat([f[0] for f in few]), ids)
+
+
 def test_rows_of_wider_buffers():
     wide = torch.randn((9, 80), generator=B.gen(3)).to(torch.float16).cuda()
     x = wide[:, 5:65]
