@@ -162,7 +162,8 @@ ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64
              EP_ERR_INVALID_ARG, "misaligned pointer");
   EP_REQUIRE(ld >= n && (!pre || ld_pre >= n) && ldq >= n && ldq_t >= m, EP_ERR_INVALID_ARG, "row stride below the row length");
   const int64_t blocks = (m + kScaleBlock - 1) / kScaleBlock;
-  EP_REQUIRE(blocks * ((n + kScaleBlock - 1) / kScaleBlock) < ((int64_t)1 << 24), EP_ERR_UNSUPPORTED, "the matrix has too many blocks for one launch");
+  EP_REQUIRE(blocks * ((n + kScaleBlock - 1) / kScaleBlock) < ((int64_t)1 << 23), EP_ERR_UNSUPPORTED,
+             "the matrix has too many blocks for one launch");  // (workgroups of 512 threads, fewer than 2^32 of those)
   EP_REQUIRE(workspace_fits(workspace, workspace_bytes, parts_bytes(blocks, n)), EP_ERR_INVALID_ARG,
              "the workspace is not 16-byte aligned or smaller than ep_epilogue_backward_fp8_workspace says");
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;

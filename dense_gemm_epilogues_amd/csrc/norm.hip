@@ -341,31 +341,33 @@ constexpr int kSumCols = 32, kSumGroups = kMaxThreads / kSumCols, kSumLoads = 8;
 __global__ __launch_bounds__(kMaxThreads) void column_sums_kernel(const float* part, int rows, int64_t ld, int cols, float* out) {
   __shared__ float red[kSumGroups][kSumCols + 1];
   const int l = (int)threadIdx.x % kSumCols, g = (int)threadIdx.x / kSumCols;
-  const int64_t c = (int64_t)blockIdx.x * kSumCols + l;
-  float s = 0.0f;
-  if (c < cols) {
-    for (int r = g; r < rows; r += kSumGroups * kSumLoads) {
-      float v[kSumLoads];
+  for (int64_t c0 = (int64_t)blockIdx.x * kSumCols; c0 < cols; c0 += (int64_t)gridDim.x * kSumCols) {
+    const int64_t c = c0 + l;
+    float s = 0.0f;
+    if (c < cols) {
+      for (int r = g; r < rows; r += kSumGroups * kSumLoads) {
+        float v[kSumLoads];
 #pragma unroll
-      for (int i = 0; i < kSumLoads; ++i) v[i] = part[min(r + i * kSumGroups, rows - 1) * ld + c];
+        for (int i = 0; i < kSumLoads; ++i) v[i] = part[min(r + i * kSumGroups, rows - 1) * ld + c];
 #pragma unroll
-      for (int i = 0; i < kSumLoads; ++i) s += r + i * kSumGroups < rows ? v[i] : 0.0f;
+        for (int i = 0; i < kSumLoads; ++i) s += r + i * kSumGroups < rows ? v[i] : 0.0f;
+      }
     }
-  }
-  red[g][l] = s;
-  __syncthreads();
-  // (a wave of the transpose: column l's groups are 32 lanes)
-  float t = red[l][g];
+    red[g][l] = s;
+    __syncthreads();
+    float t = red[l][g];  // (column g's groups are 32 lanes)
 #pragma unroll
-  for (int d = 1; d < kSumGroups; d *= 2) t += __shfl_xor(t, d);
-  const int64_t at = (int64_t)blockIdx.x * kSumCols + g;
-  if (l == 0 && at < cols) out[at] = t;
+    for (int d = 1; d < kSumGroups; d *= 2) t += __shfl_xor(t, d);
+    if (l == 0 && c0 + g < cols) out[c0 + g] = t;
+    __syncthreads();
+  }
 }
 
 }  // namespace
 
 hipError_t launch_column_sums(const float* part, int rows, int64_t ld, int cols, float* out, hipStream_t s) {
-  column_sums_kernel<<<(unsigned)((cols + kSumCols - 1) / kSumCols), kMaxThreads, 0, s>>>(part, rows, ld, cols, out);
+  const int blocks = (cols + kSumCols - 1) / kSumCols;
+  column_sums_kernel<<<(unsigned)(blocks < 1 << 16 ? blocks : 1 << 16), kMaxThreads, 0, s>>>(part, rows, ld, cols, out);
   return hipGetLastError();
 }
 

@@ -333,8 +333,8 @@ ep_status ep_matmul_fp8_epilog(int64_t m, int64_t n, int64_t k, const void* a, i
  * follow: with g = dout act'(pre) in fp32 (EP_ACT_NONE: g = dout, pre NULL; relu' is 1 where pre > 0), q (m x n) and scale
  * as ep_quantize_fp8 makes them of g with 1 x 128 blocks, q_t (n x m) and scale_t the same of its transpose, and dbias[j] =
  * sum over i of g[i][j] in fp32, in a fixed order.  The workspace (16-byte aligned, of ep_epilogue_backward_fp8_workspace bytes, none for up to
- * 128 rows) holds its partial sums.  At most 2^24 - 1
- * * blocks of 128 x 128. */
+ * 128 rows) holds its partial sums.  Fewer than 2^23
+ * blocks of 128 x 128. */
 ep_status ep_epilogue_backward_fp8_workspace(int64_t m, int64_t n, size_t* bytes);
 ep_status ep_epilogue_backward_fp8(const void* dout, int64_t m, int64_t n, int64_t ld, int elt, int activation, const void* pre,
                                    int64_t ld_pre, void* q, int64_t ldq, float* scale, void* q_t, int64_t ldq_t, float* scale_t,

@@ -211,3 +211,20 @@ def test_epilogue_abi():
         ({"g": None}, INVALID), ({"q": None}, INVALID), ({"s": None}, INVALID), ({"qt": None}, INVALID), ({"st_": None}, INVALID), ({"db": None}, INVALID),
         ({"ld": 7}, INVALID), ({"ldp": 7}, INVALID), ({"ldq": 7}, INVALID), ({"ldqt": 199}, INVALID), ({"ws": None}, INVALID), ({"wsb": 63}, INVALID),
         ({"ws": P + 8}, INVALID), ({"pre": P + 1}, INVALID), ({"m": 2 ** 20, "n": 2 ** 20, "ld": 2 ** 20, "ldp": 2 ** 20, "ldq": 2 ** 20, "ldqt": 2 ** 20}, UNSUPPORTED)))
+
+
+def test_launch_limits():
+    """The largest launches have fewer than 2^32 threads: refused at the limit, and not (but for the missing or unsuitable
+    stream, HIP's own error) below it."""
+    L = ep.lib()
+    need = ctypes.c_size_t()
+    back = lambda m, n: L.ep_epilogue_backward_fp8(P, m, n, n, 1, 0, None, 0, P, n, P, P, m, P, P, P, 1 << 62, ctypes.c_void_p(0))  # noqa: E731
+    assert back(1 << 18, 1 << 19) == UNSUPPORTED and b"blocks" in L.ep_last_error()  # 2^11 x 2^12 blocks of 512 threads
+    norm = lambda m, h: L.ep_rms_norm(P, m, h, h, 1, None, 0, P, 1, 1e-5, None, 0, P, h, None, P, None)  # noqa: E731
+    for m, h in ((1 << 22, 513), (1 << 26, 512), (1 << 28, 128)):
+        assert norm(m, h) == UNSUPPORTED and b"launch" in L.ep_last_error()
+    assert L.ep_epilogue_backward_fp8_workspace(1 << 18, 1 << 18, ctypes.byref(need)) == 0 and need.value == 4 << 29
+    if not torch.cuda.is_available():
+        assert back(1 << 18, (1 << 19) - 128) == 4
+        for m, h in (((1 << 22) - 1, 513), ((1 << 26) - 4, 512), ((1 << 28) - 16, 128)):
+            assert norm(m, h) == 4
