@@ -93,6 +93,14 @@ def matrix(name, t, dtypes, shape, device=None):
     return unit_columns(name, t)
 
 
+def vector(name, t, dtypes, n, device):
+    """check and contiguous of n values, in one look where they pass (a tuple of dtypes)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == (n,) and t.device == device and t.is_contiguous():
+        return
+    check(name, t, dtypes, (n,), device)
+    contiguous(name, t)
+
+
 def empty(shape, dtype, device, columns_outermost=False):
     """An uninitialised tensor (torch.empty takes half as long again as this); a matrix with columns_outermost as the transpose of
     a contiguous one."""
@@ -146,7 +154,7 @@ def streamed(f):
                 raise ValueError(f"the stream is on {stream.device}, {name} is on {first.device}")
             with torch.cuda.stream(stream):
                 return f(*args, **kw)
-        if first.get_device() != torch.cuda.current_device():
+        if first.get_device() != torch._C._cuda_getDevice():  # (torch.cuda.current_device without its look whether there is one)
             with torch.cuda.device(first.device):
                 return f(*args, **kw)
         return f(*args, **kw)

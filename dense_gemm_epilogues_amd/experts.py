@@ -21,7 +21,7 @@ import torch
 
 from . import _check, lib
 from ._operators import (E4M3, ELT, blocks, check, check_out, contiguous, current_stream, empty, matrix, no_gradient,
-                         on_device, streamed, unit_columns)
+                         on_device, streamed, unit_columns, vector)
 
 __all__ = ["ExpertOrder", "expert_route", "expert_route_backward", "expert_order", "expert_dispatch", "expert_combine", "expert_combine_backward"]
 
@@ -59,8 +59,7 @@ def expert_route(logits, topk, bias=None, score="softmax", groups=1, topk_groups
     if not isinstance(topk, int) or topk < 1:
         raise ValueError(f"topk must be a whole number of at least 1, got {topk}")
     if bias is not None:
-        check("bias", bias, torch.float32, (e,), logits.device)
-        contiguous("bias", bias)
+        vector("bias", bias, (torch.float32,), e, logits.device)
     no_gradient("expert_route", logits, bias)
     on_device(logits)
     dev = logits.device

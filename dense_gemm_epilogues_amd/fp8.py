@@ -22,7 +22,7 @@ import torch
 
 from . import _check, lib
 from ._operators import (BLOCK, E4M3, ELT, blocks, check, check_out, contiguous, current_stream, empty, matrix, no_gradient,
-                         on_device, streamed, unit_columns)
+                         on_device, streamed, unit_columns, vector)
 
 __all__ = ["quantize_fp8", "matmul_fp8", "EpilogueGradients", "epilogue_backward_fp8", "grouped_matmul_fp8", "grouped_wgrad_fp8"]
 
@@ -123,8 +123,7 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, bias=
     if epilog:
         act = _activation(activation)
         if bias is not None:
-            check("bias", bias, (out_dtype, torch.float32), (n,), a.device)
-            contiguous("bias", bias)
+            vector("bias", bias, (out_dtype, torch.float32), n, a.device)
             inputs += (bias,)
         if residual is not None:
             ld_res = matrix("residual", residual, (out_dtype,), (m, n), a.device)

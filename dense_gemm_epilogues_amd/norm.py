@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import _check, lib
-from ._operators import E4M3, ELT, blocks, check, contiguous, current_stream, empty, matrix, no_gradient, on_device, streamed
+from ._operators import E4M3, ELT, blocks, current_stream, empty, matrix, no_gradient, on_device, streamed, vector
 
 __all__ = ["Normed", "rms_norm", "rms_norm_backward"]
 
@@ -29,9 +29,7 @@ class Normed(NamedTuple):
     rstd: torch.Tensor
 
 
-def _weight(weight, x):
-    check("weight", weight, (x.dtype, torch.float32), (x.shape[1],), x.device)
-    contiguous("weight", weight)
+F32 = torch.float32
 
 
 @streamed
@@ -42,7 +40,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False):
     ldx = matrix("x", x, ELT, (None, None))
     m, h = x.shape
     dev = x.device
-    _weight(weight, x)
+    vector("weight", weight, (x.dtype, F32), h, dev)
     ldr = 0 if residual is None else matrix("residual", residual, (x.dtype,), (m, h), dev)
     if not 0 <= eps < float("inf"):
         raise ValueError(f"eps must be finite and not negative, got {eps}")
@@ -50,8 +48,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quantize=False):
     on_device(x)
     total = x if residual is None else empty((m, h), x.dtype, dev)
     y = empty((m, h), E4M3 if quantize else x.dtype, dev)
-    scale = empty((m, blocks(h)), torch.float32, dev, columns_outermost=True) if quantize else None
-    rstd = empty((m,), torch.float32, dev)
+    scale = empty((m, blocks(h)), F32, dev, columns_outermost=True) if quantize else None
+    rstd = empty((m,), F32, dev)
     if m and h:
         _check(lib().ep_rms_norm(x.data_ptr(), m, h, ldx, ELT[x.dtype], None if residual is None else residual.data_ptr(), ldr,
                                  weight.data_ptr(), ELT[weight.dtype], eps, total.data_ptr(), h, y.data_ptr(), h,
@@ -78,14 +76,13 @@ def rms_norm_backward(dy, x, weight, rstd, dresidual=None):
     m, h = dy.shape
     dev, same = dy.device, (dy.dtype,)
     ldx = matrix("x", x, same, (m, h), dev)
-    _weight(weight, x)
-    check("rstd", rstd, torch.float32, (m,), dev)
-    contiguous("rstd", rstd)
+    vector("weight", weight, (dy.dtype, F32), h, dev)
+    vector("rstd", rstd, (F32,), m, dev)
     ldr = 0 if dresidual is None else matrix("dresidual", dresidual, same, (m, h), dev)
     no_gradient("rms_norm_backward", dy, x, weight, rstd, dresidual)
     on_device(dy)
     dx = empty((m, h), dy.dtype, dev)
-    dweight = empty((h,), torch.float32, dev)
+    dweight = empty((h,), F32, dev)
     if not m or not h:
         return dx, dweight.zero_()
     need = _workspace(m, h)
