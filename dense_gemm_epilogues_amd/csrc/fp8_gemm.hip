@@ -341,30 +341,6 @@ __device__ __forceinline__ void store_tile(const Fp8Gemm& p, const Tile& t, int 
   }
 }
 
-// 64 columns of 16 rows in 16-bit values: a and b are a lane's 8 of its row's first and second 32, which neighbouring
-// lanes trade, so that one store writes whole lines of the even lanes' rows (at d, `rows` of them and the odd lanes'
-// inside the matrix), the other of the odd lanes'
-__device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int left, bool odd, u32x4 a, u32x4 b) {
-  u32x4 x, y;
-#pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
-    x[h] = odd ? got : a[h];
-    y[h] = odd ? b[h] : got;
-  }
-  if (left >= 8) {
-    if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)d);
-    if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(d + ld * 2));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e >= left) continue;
-      if (rows > 0) *(uint16_t*)(d + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
-      if (rows > 1) *(uint16_t*)(d + ld * 2 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
-    }
-  }
-}
-
 // The same for 16-bit outputs and rows in row_in's order: neighbouring lanes, which hold neighbouring rows,
 // first trade halves of 64 columns, so that a store instruction writes whole 128-byte lines, which leave the
 // caches to the operands (non-temporal).  The experts' weight gradients, 2.7 GB of stores: 1518 us with half
@@ -382,13 +358,27 @@ __device__ __forceinline__ void store_lines(const Fp8Gemm& p, const Tile& t, int
     const int rows = t.mv - m_at - m;
 #pragma unroll
     for (int j = 0; j < NT; j += 4) {
-      u32x4 a, b;  // the row's first and second 32 columns' pieces
+      u32x4 a, b, x, y;  // the row's first and second 32 columns' pieces; traded
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         a[h] = pack2_elt<OT>(acc[i][j + h / 2][2 * (h & 1)], acc[i][j + h / 2][2 * (h & 1) + 1]);
         b[h] = pack2_elt<OT>(acc[i][j + 2 + h / 2][2 * (h & 1)], acc[i][j + 2 + h / 2][2 * (h & 1) + 1]);
+        const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
+        x[h] = odd ? got : a[h];
+        y[h] = odd ? b[h] : got;
       }
-      store_pair(row + j * 32, p.ldd, rows, t.nv - n_at - n0 - j * 16, odd, a, b);
+      const int left = t.nv - n_at - n0 - j * 16;
+      if (left >= 8) {
+        if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)(row + j * 32));
+        if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(row + p.ldd * 2 + j * 32));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (e >= left) continue;
+          if (rows > 0) *(uint16_t*)(row + j * 32 + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+          if (rows > 1) *(uint16_t*)(row + p.ldd * 2 + j * 32 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+        }
+      }
     }
   }
 }
@@ -438,7 +428,31 @@ __device__ __forceinline__ void finish_tile(const Fp8GemmEpilog& p, const Tile& 
   }
 }
 
-// the bias is in the accumulators from the start (start_bias); at least 8 columns
+// store_lines' 64 columns of 16 rows: a and b are a lane's 8 of its row's first and second 32, which neighbouring
+// lanes trade, so that one store writes whole lines of the even lanes' rows (at d, `rows` of them and the odd lanes'
+// inside the matrix), the other of the odd lanes'
+__device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int left, bool odd, u32x4 a, u32x4 b) {
+  u32x4 x, y;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? a[h] : b[h]), 0xb1, 0xf, 0xf, true);
+    x[h] = odd ? got : a[h];
+    y[h] = odd ? b[h] : got;
+  }
+  if (left >= 8) {
+    if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)d);
+    if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(d + ld * 2));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e >= left) continue;
+      if (rows > 0) *(uint16_t*)(d + e * 2) = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+      if (rows > 1) *(uint16_t*)(d + ld * 2 + e * 2) = (uint16_t)(y[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// The bias is in the accumulators from the start (start_bias); at least 8 columns.
 template <int OT, int MT, int NT>
 __device__ __forceinline__ void finish_lines(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
   const int lane = here(lane_id());

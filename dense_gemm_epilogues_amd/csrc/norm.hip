@@ -5,7 +5,8 @@
 //   dr_j = rstd (w_j dy_j - r_j rstd mean_k(w_k dy_k r_k rstd)) + dres_j,  dw_j = sum over rows of dy_j r_j rstd
 //
 // Everything is bound by HBM: a row is read once, held in registers as fp32 while its sum is made, and written once.
-// r is what later readers see (the residual stream, the backward pass), so the norm is of the rounded r.
+// r is what later readers see (the residual stream, the backward pass), so the norm is of the rounded r.  8192 x 5120 bf16: 54 us
+// to e4m3 with a residual (295 MB, 5.4 TB/s), its gradients in 66 (336 MB, 5.1), one row in 3.5.
 #include "block_ops.hpp"
 #include "fp8_device.hpp"
 
@@ -210,7 +211,8 @@ hipError_t launch_norm_e(const NormArgs& p, hipStream_t s) {
 
 // ------------------------------------------------------------------------------------- gradients
 // A workgroup takes the rows blockIdx.x, blockIdx.x + strips, ... and keeps its part of dw in registers; the parts are
-// summed by a second launch in a fixed order.
+// summed by a second launch in a fixed order.  (The next row's loads issued ahead take registers that other workgroups hide them
+// with: 78 us for 8192 x 5120 instead of 66; 256 strips 77, 768 as well.)
 template <int E, int CH, int ENDS>
 __global__ __launch_bounds__(kMaxThreads) void norm_back_kernel(NormBackArgs p) {
   __shared__ float red[2][kMaxThreads / 64];
