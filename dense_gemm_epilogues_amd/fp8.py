@@ -102,7 +102,7 @@ def matmul_fp8(a, a_scale, b, b_scale, out_dtype=torch.bfloat16, out=None, bias=
 
     With an epilogue, p = a b^T + bias and the result is act(p) + residual, in fp32 before its one rounding: bias (N; out_dtype or
     float32), activation "relu", "gelu" (exact) or "silu", residual (M x N; out_dtype).  `out` may be the residual itself.  save_pre
-    returns (result, p), p rounded to out_dtype, for epilogue_backward_fp8.
+    returns (result, p), p rounded to out_dtype, for epilogue_backward_fp8.  (With an epilogue K is at least 16.)
 
     16-bit outputs of more than 8 rows and K over 256 pass the e4m3 matrix instruction, which adds the products of 8
     neighbouring k in fixed point before fp32: each loses less than 2^-13 of the largest of the 8 (of normal

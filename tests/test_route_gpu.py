@@ -81,6 +81,41 @@ def test_masked_experts(kw):
     assert (order.pos[:2] == -1).all()
 
 
+@pytest.mark.parametrize("t,e,topk,kw", [(5, 900, 7, {"groups": 3, "topk_groups": 2}), (4, 1023, 9, {"groups": 33, "topk_groups": 5, "score": "sigmoid", "bias": 1}),
+                                         (3, 770, 3, {"groups": 5, "topk_groups": 1, "group_top": 1}), (4100, 300, 4, {"groups": 3, "topk_groups": 1})])
+def test_groups_that_do_not_divide_a_wave(t, e, topk, kw):
+    """Up to 32 experts a lane; equal and masked ones among them."""
+    g = B.gen(e)
+    logits = (2 * torch.randn((t, e), generator=g)).clamp(-8, 8)
+    logits[1] = logits[1].round()
+    logits[2, ::3] = -math.inf
+    kw = dict(kw)
+    if "bias" in kw:
+        kw["bias"] = 0.1 * torch.randn(e, generator=g)
+    check_route(logits, topk, **kw)
+
+
+@pytest.mark.parametrize("t", [3, 5000])
+def test_zeros_of_either_sign_are_equal(t):
+    logits = torch.zeros((t, 40))
+    logits[:, ::2] = -0.0
+    ids, _ = check_route(logits, 5)
+    assert (ids.cpu() == torch.arange(5)).all()
+    ids, _ = check_route(logits, 5, score="sigmoid", bias=-0.5 * torch.ones(40))  # (keys of 0)
+    assert (ids.cpu() == torch.arange(5)).all()
+
+
+@pytest.mark.parametrize("t", [6, 4200])
+def test_keys_that_fp32_makes_equal(t):
+    """Neighbours far closer than fp32's step, in every order, inside and at the end of the choice: decided in double."""
+    logits = torch.full((t, 48), 20.0)  # sigmoid: 1 - 2e-9, the others' differences are below 2e-9
+    for i in range(t):
+        logits[i, torch.randperm(48, generator=B.gen(i))] = 18 + 6 * torch.arange(48) / 48
+    check_route(logits, 6, score="sigmoid", bias=torch.zeros(48))
+    check_route(logits, 6, score="sigmoid", groups=4, topk_groups=2)
+    check_route(logits, 48, score="sigmoid", bias=torch.zeros(48))
+
+
 def test_far_logits():
     """Scores that underflow in fp32 still decide: keys are in double, and no weight is NaN."""
     logits = torch.tensor([[-200.0, -201.0, -199.0, -300.0], [30.0, 31.0, 32.0, 29.0], [200.0, -200.0, 0.0, 1.0], [-4000.0, -4001.0, -3999.0, -4002.0]])
