@@ -70,7 +70,7 @@ ep_status ep_rms_norm_backward_workspace(int64_t m, int64_t h, size_t* bytes) {
   api_clear();
   EP_REQUIRE(bytes, EP_ERR_INVALID_ARG, "null pointer");
   *bytes = 0;
-  if (m >= 1 && h >= 1 && m < kMaxCount && h < kMaxFeatures) *bytes = parts_bytes(norm_back_strips(m), h);
+  if (m >= 1 && h >= 1 && m < kMaxCount && h < kMaxFeatures) *bytes = parts_bytes(norm_back_strips(m, h), h);
   return EP_OK;
 }
 
@@ -85,7 +85,7 @@ ep_status ep_rms_norm_backward(const void* dy, int64_t m, int64_t h, int64_t ld_
   EP_REQUIRE(aligned(dy, size) && aligned(x, size) && aligned(dresidual, size) && aligned(dx, size) && aligned(rstd, 4) &&
                  aligned(dweight, 4), EP_ERR_INVALID_ARG, "misaligned pointer");
   EP_REQUIRE(ld_dy >= h && ldx >= h && ld_dx >= h && (!dresidual || ld_dres >= h), EP_ERR_INVALID_ARG, "row stride below the row length");
-  const int strips = norm_back_strips(m);
+  const int strips = norm_back_strips(m, h);
   EP_REQUIRE(workspace_fits(workspace, workspace_bytes, parts_bytes(strips, h)), EP_ERR_INVALID_ARG,
              "the workspace is not 16-byte aligned or smaller than ep_rms_norm_backward_workspace says");
   if ((st = (ep_status)api_stream(stream)) != EP_OK) return st;

@@ -36,7 +36,7 @@ struct NormBackArgs {
   int w32;
   int strips;                        // workgroups the rows are dealt out to
 };
-int norm_back_strips(int64_t m);
+int norm_back_strips(int64_t m, int64_t h);
 hipError_t launch_rms_norm_backward(int elt, const NormBackArgs& p, hipStream_t s);
 
 // out[c] = sum over rows of part[row][c], rows ld apart, in a fixed order

@@ -7,6 +7,8 @@
 // Everything is bound by HBM: a row is read once, held in registers as fp32 while its sum is made, and written once.
 // r is what later readers see (the residual stream, the backward pass), so the norm is of the rounded r.  8192 x 5120 bf16: 54 us
 // to e4m3 with a residual (295 MB, 5.4 TB/s), its gradients in 66 (336 MB, 5.1), one row in 3.5.
+#include <algorithm>
+
 #include "block_ops.hpp"
 #include "fp8_device.hpp"
 
@@ -316,20 +318,32 @@ __global__ __launch_bounds__(256) void norm_back_long_weight_kernel(NormBackArgs
   store8<EL_F32>((char*)(p.part + (int64_t)blockIdx.y * p.h + c), n, dw);
 }
 
+// Threads a row takes and the times 8 values each of them holds: 1, 2 in whole rows, 0 in rows too long for that
+struct BackShape {
+  int threads, chunks;
+};
+BackShape back_shape(int64_t h) {
+  const int64_t lanes = (h + 7) / 8;
+  if (lanes <= kMaxThreads) return {(int)((lanes + 63) / 64 * 64), 1};
+  if (h % 8 == 0 && lanes <= 2 * kMaxThreads) return {(int)((lanes + 127) / 128 * 64), 2};
+  return {kMaxThreads, 0};
+}
+
 template <int E>
 hipError_t launch_back(const NormBackArgs& p, hipStream_t s) {
-  const int lanes = (p.h + 7) / 8;
-  const int threads = (lanes + 63) / 64 * 64;
-  if (p.h < 8) {
-    norm_back_kernel<E, 1, ANY><<<(unsigned)p.strips, threads, 0, s>>>(p);
-  } else if (lanes <= kMaxThreads) {
-    if (p.h % 8 == 0) norm_back_kernel<E, 1, WHOLE><<<(unsigned)p.strips, threads, 0, s>>>(p);
-    else norm_back_kernel<E, 1, CUT><<<(unsigned)p.strips, threads, 0, s>>>(p);
-  } else if (p.h % 8 == 0 && lanes <= 2 * kMaxThreads) {
-    norm_back_kernel<E, 2, WHOLE><<<(unsigned)p.strips, (threads / 2 + 63) / 64 * 64, 0, s>>>(p);
-  } else {
+  const BackShape shape = back_shape(p.h);
+  const unsigned strips = (unsigned)p.strips, threads = (unsigned)shape.threads;
+  if (shape.chunks == 0) {
     norm_back_long_kernel<E><<<(unsigned)p.m, kMaxThreads, 0, s>>>(p);
-    norm_back_long_weight_kernel<E><<<dim3((unsigned)((lanes + 255) / 256), (unsigned)p.strips), 256, 0, s>>>(p);
+    norm_back_long_weight_kernel<E><<<dim3((unsigned)(((p.h + 7) / 8 + 255) / 256), strips), 256, 0, s>>>(p);
+  } else if (shape.chunks == 2) {
+    norm_back_kernel<E, 2, WHOLE><<<strips, threads, 0, s>>>(p);
+  } else if (p.h < 8) {
+    norm_back_kernel<E, 1, ANY><<<strips, threads, 0, s>>>(p);
+  } else if (p.h % 8 == 0) {
+    norm_back_kernel<E, 1, WHOLE><<<strips, threads, 0, s>>>(p);
+  } else {
+    norm_back_kernel<E, 1, CUT><<<strips, threads, 0, s>>>(p);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.strips == 1) return e;
@@ -379,10 +393,23 @@ hipError_t launch_rms_norm(int elt, const NormArgs& p, hipStream_t s) {
   return launch_norm_e<EL_F32>(p, s);
 }
 
-// As many workgroups as walk the rows evenly, at most 512 (two on each compute unit)
-int norm_back_strips(int64_t m) {
-  constexpr int64_t kStrips = 512;
-  const int64_t each = (m + kStrips - 1) / kStrips;
+// How many workgroups the rows are dealt out to.  More of them hide each other's loads, up to 24 waves a compute unit and as many
+// workgroups on each; each brings a part of dw to be written and summed, which pays from 4 rows on, and a second one on
+// a unit from 2 on, for rows of more than 128 threads only where there are 3 for each unit.  bf16 with dres, us:
+//   16384 x 256: 21 with 2048 workgroups, 42 with 512;  16384 x 1024: 31, 47;  16384 x 2048: 52 with 1024, 72 with 512;
+//   8192 x 5120: 66 with 512, 77 with 256, 768 or 1024;  512 x 5120: 11.2 with 256, 13.2 with 512;
+//   1000 x 12288: 26 with 256, 30 with 512;  1000 x 1024: 8.5 with 512, 10.1 with 1000.
+int norm_back_strips(int64_t m, int64_t h) {
+  constexpr int64_t kUnits = 256;
+  const BackShape shape = back_shape(h);
+  const int held = shape.threads * shape.chunks;  // 8 values each
+  int64_t most = 8 * kUnits, least = 2 * kUnits;
+  if (held == 0) most = least;
+  while (most > kUnits && most / kUnits * held > 1536) most /= 2;
+  if (held > 128 && m < 3 * kUnits) least = kUnits;
+  const int64_t wanted = std::max(m / 4, least);
+  const int64_t strips = std::min(most, wanted + wanted / 16);  // (a few more rather than a row more for each; past `most` they would queue)
+  const int64_t each = (m + strips - 1) / strips;
   return (int)((m + each - 1) / each);
 }
 
