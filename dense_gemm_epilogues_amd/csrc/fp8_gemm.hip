@@ -386,6 +386,14 @@ __device__ __forceinline__ void store_lines(const Fp8Gemm& p, const Tile& t, int
 // Fewer than 8 columns, with an epilogue (a type of its own, which chooses finish_narrow: in the same kernel it
 // takes registers from finish_lines): they lie in one place of 16 lanes
 struct Fp8GemmNarrow : Fp8GemmEpilog {};
+// Rows of D or P that are not whole lines of 128 bytes, so that neighbouring tiles share some: written through the caches, which
+// join them (another type, again for its registers).  bf16 with P: 6842 x 2203 x 528 in 26 us, 45 with non-temporal stores; 4099 x 5001 x
+// 2048 in 74, 108.  Whole lines: 8192 x 4096 x 512 with bias, GELU, P and residual in 64 us, 52 with non-temporal stores.
+struct Fp8GemmShared : Fp8GemmEpilog {};
+inline bool whole_lines(const Fp8GemmEpilog& p, int size) {
+  auto whole = [&](const void* at, int64_t ld) { return (((uintptr_t)at | (uint64_t)ld * size) & 127) == 0; };
+  return whole(p.d, p.ldd) && (!p.e.pre || whole(p.e.pre, p.e.ld_pre));
+}
 template <int OT, int MT, int NT>
 __device__ __forceinline__ void finish_narrow(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
   const int lane = here(lane_id());
@@ -431,6 +439,7 @@ __device__ __forceinline__ void finish_tile(const Fp8GemmEpilog& p, const Tile& 
 // store_lines' 64 columns of 16 rows: a and b are a lane's 8 of its row's first and second 32, which neighbouring
 // lanes trade, so that one store writes whole lines of the even lanes' rows (at d, `rows` of them and the odd lanes'
 // inside the matrix), the other of the odd lanes'
+template <bool WHOLE>
 __device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int left, bool odd, u32x4 a, u32x4 b) {
   u32x4 x, y;
 #pragma unroll
@@ -440,8 +449,13 @@ __device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int le
     y[h] = odd ? b[h] : got;
   }
   if (left >= 8) {
-    if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)d);
-    if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(d + ld * 2));
+    if constexpr (WHOLE) {
+      if (rows > 0) __builtin_nontemporal_store(x, (u32x4_u*)d);
+      if (rows > 1) __builtin_nontemporal_store(y, (u32x4_u*)(d + ld * 2));
+    } else {
+      if (rows > 0) *(u32x4_u*)d = x;
+      if (rows > 1) *(u32x4_u*)(d + ld * 2) = y;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -453,7 +467,7 @@ __device__ __forceinline__ void store_pair(char* d, int64_t ld, int rows, int le
 }
 
 // The bias is in the accumulators from the start (start_bias); at least 8 columns.
-template <int OT, int MT, int NT>
+template <int OT, bool WHOLE, int MT, int NT>
 __device__ __forceinline__ void finish_lines(const Fp8GemmEpilog& p, const Tile& t, int m_at, int n_at, f32x4 (&acc)[MT][NT]) {
   const int lane = here(lane_id());
   const bool odd = lane & 1;
@@ -489,7 +503,7 @@ __device__ __forceinline__ void finish_lines(const Fp8GemmEpilog& p, const Tile&
           const f32x4 v = acc[i][j + 2 * u + h / 2];
           out[u][h] = pack2_elt<OT>(v[2 * (h & 1)], v[2 * (h & 1) + 1]);
         }
-      store_pair((char*)p.e.pre + (row * p.e.ld_pre + t.n0 + n) * 2, p.e.ld_pre, rows, left, odd, out[0], out[1]);
+      store_pair<WHOLE>((char*)p.e.pre + (row * p.e.ld_pre + t.n0 + n) * 2, p.e.ld_pre, rows, left, odd, out[0], out[1]);
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -504,7 +518,7 @@ __device__ __forceinline__ void finish_lines(const Fp8GemmEpilog& p, const Tile&
 #pragma unroll
       for (int h = 0; h < 4; ++h) out[u][h] = pack2_elt<OT>(f[2 * h], f[2 * h + 1]);
     }
-    store_pair((char*)p.d + (row * p.ldd + t.n0 + n) * 2, p.ldd, rows, left, odd, out[0], out[1]);
+    store_pair<WHOLE>((char*)p.d + (row * p.ldd + t.n0 + n) * 2, p.ldd, rows, left, odd, out[0], out[1]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
@@ -690,8 +704,9 @@ void fp8_tile_kernel(Args p) {
     t_last = 0.0f;
   };
 
+  constexpr bool kLines = std::is_same_v<Args, Fp8GemmEpilog> || std::is_same_v<Args, Fp8GemmShared>;
   auto start = [&](const Tile& t) __attribute__((always_inline)) {
-    if constexpr (std::is_same_v<Args, Fp8GemmEpilog>) start_bias<OT>(args_here<Args>(), t, wn * WTN, acc);
+    if constexpr (kLines) start_bias<OT>(args_here<Args>(), t, wn * WTN, acc);
   };
 
   Tile cur, ahead;
@@ -820,7 +835,7 @@ void fp8_tile_kernel(Args p) {
       if (!more) __builtin_amdgcn_s_waitcnt(0x0070);
       add_last();
       if constexpr (std::is_same_v<Args, Fp8GemmNarrow>) finish_narrow<OT>(args_here<Args>(), cur, wm * WTM, wn * WTN, acc);
-      else if constexpr (std::is_same_v<Args, Fp8GemmEpilog>) finish_lines<OT>(args_here<Args>(), cur, wm * WTM, wn * WTN, acc);
+      else if constexpr (kLines) finish_lines<OT, std::is_same_v<Args, Fp8GemmEpilog>>(args_here<Args>(), cur, wm * WTM, wn * WTN, acc);
       else if constexpr (OT == EL_F32) store_tile<MODE, OT, true>(args_here(), cur, wm * WTM, wn * WTN, acc);
       else store_lines<MODE, OT>(args_here(), cur, wm * WTM, wn * WTN, acc);
       done = !more;
@@ -1133,6 +1148,17 @@ hipError_t launch_wide(Args& p, hipStream_t s) {
 }
 
 template <int MODE, int OT, class Args>
+hipError_t launch_sized(Args& p, hipStream_t s) {
+  // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 36 us
+  // with operands that no cache holds, 59 with 80 large tiles); with more the large ones, which read half as much
+  // through the caches (8192 x 17408 x 5120: 602 us, 744 with small ones)
+  const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
+  // so with few rows an expert: 64 experts of 64 rows, n 4096, k 5120: 244 us, 267 with large tiles (of 128: 282, 281)
+  if (big < p.cus || (MODE == GM_GROUPED && p.M <= 96 * (int64_t)p.experts)) return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(p, s);
+  return launch_tile<MODE, OT, 256, 256, 4, 2, 1>(p, s);
+}
+
+template <int MODE, int OT, class Args>
 hipError_t launch_tiles(Args& p, hipStream_t s) {
   if constexpr (MODE == GM_MATMUL) {
     if (p.splits > 1) {
@@ -1153,14 +1179,12 @@ hipError_t launch_tiles(Args& p, hipStream_t s) {
           Fp8GemmNarrow q{p};
           return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(q, s);
         }
+        if (!whole_lines(p, elt_size(OT))) {
+          Fp8GemmShared q{p};
+          return launch_sized<MODE, OT>(q, s);
+        }
       }
-      // fewer 256 x 256 tiles than compute units: 128 x 128 ones, two workgroups a unit (777 x 5003 x 4112: 36 us
-      // with operands that no cache holds, 59 with 80 large tiles); with more the large ones, which read half as much
-      // through the caches (8192 x 17408 x 5120: 602 us, 744 with small ones)
-      const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256) * (MODE == GM_WGRAD ? p.experts : 1);
-      // so with few rows an expert: 64 experts of 64 rows, n 4096, k 5120: 244 us, 267 with large tiles (of 128: 282, 281)
-      if (big < p.cus || (MODE == GM_GROUPED && p.M <= 96 * (int64_t)p.experts)) return launch_tile<MODE, OT, 128, 128, 2, 2, 2>(p, s);
-      return launch_tile<MODE, OT, 256, 256, 4, 2, 1>(p, s);
+      return launch_sized<MODE, OT>(p, s);
     }
   }
   return launch_wide<MODE, OT>(p, s);
