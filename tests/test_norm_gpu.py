@@ -170,3 +170,11 @@ def test_graph_and_streams():
         assert torch.equal(out.y.view(torch.uint8), want.y.view(torch.uint8)) and torch.equal(out.scale, want.scale)
         assert torch.equal(out.residual, want.residual) and all(torch.equal(a, b) for a, b in zip(back, grads))
         assert all(torch.equal(a, b) for a, b in zip(side, other))
+
+
+@pytest.mark.parametrize("m,h", [(257, 7000), (300, 8192), (513, 8200), (767, 1032), (769, 1032), (1500, 2048), (4100, 72), (9000, 264)])
+def test_norm_backward_by_the_number_of_workgroups(m, h):
+    """1 to 8 rows a workgroup, 256 to 2048 workgroups.  A thread of the parts' sum adds at most 2048 / 32 of them and 5 lanes' sums, a
+    workgroup ceil(m / 256) rows of 7000 and more, ceil(m / 512) of others: fewer adds than the bound counts."""
+    test_norm_backward(torch.bfloat16, m, h)
+    test_norm_backward(torch.float32, m, h)
